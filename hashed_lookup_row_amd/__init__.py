@@ -88,6 +88,13 @@ def load_library():
             "mpzch_lookup_or_insert_static": (i32, [p, p, p, i64, i32, i64, p, i64, i64, i32, p, p, p, p, p]),
             "memory_layer_step_workspace_init": (i32, [p, sz, p, sz, i64, i64, p]),
             "memory_layer_step_mark_written": (i32, [p, sz, i64, i64, i64, p, p, p, p]),
+            "hist_plan": (i32, [p, p, i64, p, i64, p, i64, i64, i64, p, p, p, p, p]),
+            "hist_append": (i32, [p, p, p, p, i64, i64, i64, i64, p, p, i32, i64, i64, i64, i64, p, i64, p]),
+            "hist_read": (i32, [p, p, p, p, i64, i64, i64, i64, p, i64, p, p, i32, p]),
+            "hist_attention_workspace_size": (sz, [i64, i64, i64, i64, i64, i64, i64]),
+            "hist_attention": (i32, [p, i32, i64, i64, i64, i64, p, p, p, p, i64, i64, i64, i64, p, i64, p, p, i64, i64,
+                                     i64, f32, i32, i64, p, p, p, sz, p]),
+            "sample_scores": (i32, [p, i32, i64, i64, i64, p, i64, p, p, p, p, p, p, p]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -107,7 +114,8 @@ def exported_symbols():
             "dks_gather_rows", "memory_layer_step",
             "memory_layer_step_workspace_size", "memory_layer_step_workspace_init", "memory_layer_step_mark_written",
             "mpzch_lookup_or_insert_static_max_n", "mpzch_lookup_or_insert_static", "ema_update_plan_subset", "ema_update_apply_batch",
-            "writeback_apply_batch", "ema_update_pair_workspace_size", "ema_update_plan_pair", "ema_update_apply_pairs"]
+            "writeback_apply_batch", "ema_update_pair_workspace_size", "ema_update_plan_pair", "ema_update_apply_pairs",
+            "hist_plan", "hist_append", "hist_read", "hist_attention_workspace_size", "hist_attention", "sample_scores"]
 
 
 def _check(rc: int, what: str):
@@ -654,3 +662,190 @@ def dks_rehash(keys, krows, new_cap, stream=None):
     _check(lib.dks_rehash(_ptr(keys), _ptr(krows), keys.numel(), _ptr(nk), _ptr(nr), int(new_cap),
                           _stream(keys.device, stream)), "dks_rehash")
     return nk, nr
+
+
+# ------------------------------------------ a history held in 8 bits, and sampling
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _vectors(t, name, heads=None, dim=None):
+    """[tokens, heads, dim] in fp32, bf16 or fp16 with contiguous elements: its type code and strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda:
+        raise HLRError(f"{name} must be a GPU tensor (got {t.device}); there is no CPU path")
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] == 0 or (heads is not None and t.shape[1] != heads) or \
+            (dim is not None and t.shape[2] != dim):
+        raise HLRError(f"{name} must be [tokens, heads, dim] with the cache's sizes (got {tuple(t.shape)})")
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise HLRError(f"the elements of {name} must be contiguous")
+    return code, s0, s1
+
+
+def _cache(k_codes, v_codes, k_scale, v_scale):
+    """(num_blocks, heads, block, dim) of a history cache, with its shapes checked."""
+    _dev(k_codes, "k_codes", torch.int8)
+    _dev(v_codes, "v_codes", torch.int8)
+    _dev(k_scale, "k_scale", torch.float32)
+    _dev(v_scale, "v_scale", torch.float32)
+    if k_codes.dim() != 4:
+        raise HLRError("k_codes must be [blocks, heads, block, dim]")
+    nb, heads, block, dim = k_codes.shape
+    if v_codes.shape != (nb, heads, block // 16, dim, 16):
+        raise HLRError("v_codes must be [blocks, heads, block / 16, dim, 16]")
+    if k_scale.shape != (nb, heads) or v_scale.shape != (nb, heads):
+        raise HLRError("k_scale and v_scale must be [blocks, heads]")
+    return nb, heads, block, dim
+
+
+def hist_plan(cached, new, block_table, free_blocks, block, max_tokens, out=None, stream=None):
+    """Block table entries and slots of a batch's new tokens.  cached, new: int32 [requests]; block_table int32
+    [requests, columns], updated in place; free_blocks int32.  Returns (slots int64 [max_tokens], cu int32
+    [requests + 1], lengths int32 [requests], counts int64 [2]: blocks taken, tokens without a block); out: the
+    same four tensors to write to."""
+    lib = load_library()
+    for t, name in ((cached, "cached"), (new, "new"), (block_table, "block_table"), (free_blocks, "free_blocks")):
+        _dev(t, name, torch.int32)
+    dev, n = cached.device, cached.numel()
+    if new.numel() != n or block_table.dim() != 2 or block_table.shape[0] != n:
+        raise HLRError("cached, new and block_table must have one entry (row) per request")
+    if out is None:
+        out = (torch.empty(int(max_tokens), dtype=torch.int64, device=dev),
+               torch.empty(n + 1, dtype=torch.int32, device=dev), torch.empty(n, dtype=torch.int32, device=dev),
+               torch.empty(2, dtype=torch.int64, device=dev))
+    else:
+        for t, name, dt, size in zip(out, ("slots", "cu", "lengths", "counts"),
+                                     (torch.int64, torch.int32, torch.int32, torch.int64), (max_tokens, n + 1, n, 2)):
+            _dev(t, name, dt)
+            if t.numel() < size:
+                raise HLRError(f"{name} must hold {size} entries")
+    slots, cu, lengths, counts = out
+    _check(lib.hist_plan(cached.data_ptr(), new.data_ptr(), n, block_table.data_ptr(), block_table.shape[1],
+                         free_blocks.data_ptr(), free_blocks.numel(), block, max_tokens, slots.data_ptr(),
+                         cu.data_ptr(), lengths.data_ptr(), counts.data_ptr(), _stream(dev, stream)), "hist_plan")
+    return slots, cu, lengths, counts
+
+
+def hist_append(k_codes, v_codes, k_scale, v_scale, k, v, slots, stream=None):
+    """Quantises keys and values [tokens, heads, dim] into the cache (in place) at `slots` (int64 [tokens])."""
+    lib = load_library()
+    nb, heads, block, dim = _cache(k_codes, v_codes, k_scale, v_scale)
+    code, kt, kh = _vectors(k, "k", heads, dim)
+    vcode, vt, vh = _vectors(v, "v", heads, dim)
+    _dev(slots, "slots", torch.int64)
+    n = k.shape[0]
+    if vcode != code or v.shape[0] != n or slots.numel() != n:
+        raise HLRError("k and v must have one type, and k, v and slots one entry per token")
+    _check(lib.hist_append(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, heads,
+                           block, dim, k.data_ptr(), v.data_ptr(), code, kt, kh, vt, vh, slots.data_ptr(), n,
+                           _stream(k.device, stream)), "hist_append")
+
+
+def hist_read(k_codes, v_codes, k_scale, v_scale, slots, dtype=torch.float32, out=None, stream=None):
+    """The keys and values that slots hold: (k, v), each [tokens, heads, dim] of `dtype`."""
+    lib = load_library()
+    nb, heads, block, dim = _cache(k_codes, v_codes, k_scale, v_scale)
+    _dev(slots, "slots", torch.int64)
+    if dtype not in _TYPES:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    n = slots.numel()
+    if out is None:
+        out = tuple(torch.empty((n, heads, dim), dtype=dtype, device=slots.device) for _ in range(2))
+    for t in out:
+        _dev(t, "out", dtype)
+        if t.numel() != n * heads * dim:
+            raise HLRError("out must hold tokens x heads x dim values")
+    k, v = out
+    _check(lib.hist_read(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, heads,
+                         block, dim, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), _TYPES[dtype],
+                         _stream(slots.device, stream)), "hist_read")
+    return k, v
+
+
+def hist_attention_workspace_size(tokens, requests, q_heads, kv_heads, dim, max_q, max_len) -> int:
+    return int(load_library().hist_attention_workspace_size(int(tokens), int(requests), int(q_heads), int(kv_heads),
+                                                            int(dim), int(max_q), int(max_len)))
+
+
+def hist_attention(q, k_codes, v_codes, k_scale, v_scale, block_table, lengths, cu, max_q, max_len, scale=None,
+                   causal=True, window=0, return_lse=False, out=None, ws=None, stream=None):
+    """softmax(scale q K^T) V of ragged queries [tokens, q_heads, dim] over the cache (include/hlr.h).  scale: default
+    dim ** -0.5.  ws: optional caller workspace (new_workspace()); default: the per-device shared buffer (calls that
+    share it must be ordered on one stream).  Returns out [tokens, q_heads, dim], or (out, lse fp32 [tokens, q_heads])."""
+    lib = load_library()
+    nb, kv_heads, block, dim = _cache(k_codes, v_codes, k_scale, v_scale)
+    code, qt, qh = _vectors(q, "q", None, dim)
+    _dev(block_table, "block_table", torch.int32)
+    _dev(lengths, "lengths", torch.int32)
+    _dev(cu, "cu", torch.int32)
+    tokens, heads, n = q.shape[0], q.shape[1], lengths.numel()
+    if heads % kv_heads != 0:
+        raise HLRError("q's heads must be a multiple of the cache's")
+    if block_table.dim() != 2 or block_table.shape[0] != n or cu.numel() != n + 1:
+        raise HLRError("block_table must have a row per request, and cu one entry more than requests")
+    dev = q.device
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
+    else:
+        _dev(out, "out", q.dtype)
+        if out.numel() != q.numel():
+            raise HLRError("out must hold tokens x heads x dim values")
+    lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
+    need = lib.hist_attention_workspace_size(tokens, n, heads, kv_heads, dim, max_q, max_len)
+    if need == 0:
+        w, wb = None, 0
+    elif ws is not None:
+        w, wb = _own_ws(ws, need)
+    else:
+        w, wb = _ws_args(dev, need)
+    _check(lib.hist_attention(q.data_ptr(), code, tokens, heads, qt, qh, k_codes.data_ptr(), v_codes.data_ptr(),
+                              k_scale.data_ptr(), v_scale.data_ptr(), nb, kv_heads, block, dim, block_table.data_ptr(),
+                              block_table.shape[1], lengths.data_ptr(), cu.data_ptr(), n, max_q, max_len,
+                              dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+                              lse.data_ptr() if return_lse else None, w, wb, _stream(dev, stream)), "hist_attention")
+    return (out, lse) if return_lse else out
+
+
+def _per_row(t, name, dtype, rows):
+    if t is None:
+        return None
+    _dev(t, name, dtype)
+    if t.numel() != rows:
+        raise HLRError(f"{name} must hold one entry per row")
+    return t.data_ptr()
+
+
+def sample_scores(scores, noise, temperature=None, top_k=None, top_p=None, min_p=None, out=None, stream=None):
+    """One item per row of scores [rows, items] (fp32, bf16 or fp16; rows may be strided), from Exp(1) noise
+    (fp32 [rows, items]); temperature, top_p, min_p: fp32 [rows], top_k: int32 [rows], or None.  Returns
+    (index int64 [rows], logprob fp32 [rows])."""
+    lib = load_library()
+    for t, name in ((scores, "scores"), (noise, "noise")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if not t.is_cuda:
+            raise HLRError(f"{name} must be a GPU tensor (got {t.device}); there is no CPU path")
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise HLRError(f"{name} must be [rows, items] with contiguous items")
+    code = _TYPES.get(scores.dtype)
+    if code is None:
+        raise TypeError(f"scores must be float32, bfloat16 or float16, got {scores.dtype}")
+    if noise.dtype != torch.float32 or noise.shape != scores.shape:
+        raise HLRError("noise must be float32 of the scores' shape")
+    rows, items = scores.shape
+    dev = scores.device
+    index, logprob = out if out is not None else (torch.empty(rows, dtype=torch.int64, device=dev),
+                                                  torch.empty(rows, dtype=torch.float32, device=dev))
+    if out is not None:
+        _per_row(index, "out index", torch.int64, rows)
+        _per_row(logprob, "out logprob", torch.float32, rows)
+    _check(lib.sample_scores(scores.data_ptr(), code, rows, items, scores.stride(0), noise.data_ptr(), noise.stride(0),
+                             _per_row(temperature, "temperature", torch.float32, rows),
+                             _per_row(top_k, "top_k", torch.int32, rows), _per_row(top_p, "top_p", torch.float32, rows),
+                             _per_row(min_p, "min_p", torch.float32, rows), index.data_ptr(), logprob.data_ptr(),
+                             _stream(dev, stream)), "sample_scores")
+    return index, logprob

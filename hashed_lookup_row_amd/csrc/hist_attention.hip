@@ -1,0 +1,610 @@
+// Attention over the 8-bit history cache: out = softmax(s q K^T) V for ragged
+// requests, with keys and values as codes times a scale per block and head.
+//
+// Everything one wave does is a tile of 64 tokens (four chunks of 16) against
+// 16 query rows, in registers:
+//   S^T = K Q^T   v_mfma_f32_16x16x32_f16, A = codes as f16 (exact: they are
+//                 whole numbers up to 127), B = the queries
+//   O^T = V^T P^T with the scores' own registers as the B operand
+// The tokens that lane group g (= lane/16) holds after the first product are
+// exactly chunk g: the rows of the A operand are given to lanes in the order
+// token(t, m) = 16 (m/4) + 4 t + m%4, so the second product's operand needs no
+// exchange between lanes, and each lane has one key scale and one value scale
+// (a block holds whole chunks).  A lane's value operand for one d is the 16
+// bytes of [chunk][d][16].
+//
+// Precision: a query row is multiplied by a power of two that brings its
+// largest magnitude to [512, 1024), so bf16 and f16 queries are exact in f16
+// (fp32 ones are split into two f16 parts).  Scores, the running maximum and
+// sum, and the output are fp32.  The weights p are one f16 part for bf16
+// outputs and two for fp16 and fp32: at 11 bits their own rounding would be as
+// large as fp16's (the error against 64 bits 1.4 to 1.5 times what the output's rounding gives).  A
+// weight enters the second product times its chunk's value scale, relative to
+// the row's largest such product so far and times 2^12, which keeps terms
+// down to 2^-23 of the largest in f16's normal range.  Running maxima are whole
+// numbers (in log2), so rescaling and joining waves and splits is exact.
+#include "hlr_common.hpp"
+#include "hist_common.hpp"
+
+#include <type_traits>
+
+namespace {
+using namespace hlr;
+
+typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTile = 64;      // tokens of a tile
+constexpr int kWaves = 4;      // waves of a block
+constexpr float kNone = -3.0e38f;  // running maxima of a row that has seen nothing
+constexpr float kUp = 12.f;    // weights are held as 2^kUp p
+constexpr float kSlack = 3.f;  // a running maximum follows once scores pass it by this (in log2)
+
+struct Args {
+  const void *q;
+  int64_t q_tok, q_head;  // strides, elements
+  const int8_t *k, *v;
+  const float *ks, *vs;
+  const int *table;
+  int64_t cols;
+  const int *lengths, *cu;
+  void *out;
+  float *lse;        // nullable
+  float *part;       // [splits][tokens][heads][D], when split
+  float2 *part_ml;   // [splits][tokens][heads]: running maximum and sum
+  int64_t tokens, num_blocks;
+  int kv_heads, group, log_b;
+  int causal, window;
+  float scale;       // softmax scale times log2(e)
+  int chunk;         // tokens of a split
+  int row_tiles;     // blocks of rows per request
+  int max_q, max_len;  // the caller's bounds: what a launch covers
+};
+
+__device__ __forceinline__ h8 f16_of_codes(uint32_t lo, uint32_t hi) {
+  // byte b -> f16 with bits 0x64xx = 1024 + (b ^ 0x80) = 1152 + code
+  lo ^= 0x80808080u;
+  hi ^= 0x80808080u;
+  const uint32_t w[4] = {
+      __builtin_amdgcn_perm(0x64646464u, lo, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, lo, 0x04030402u),
+      __builtin_amdgcn_perm(0x64646464u, hi, 0x04010400u), __builtin_amdgcn_perm(0x64646464u, hi, 0x04030402u)};
+  const h2 bias = {static_cast<_Float16>(1152.f), static_cast<_Float16>(1152.f)};
+  h8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const h2 x = __builtin_bit_cast(h2, w[i]) - bias;
+    r[2 * i] = x[0];
+    r[2 * i + 1] = x[1];
+  }
+  return r;
+}
+
+__device__ __forceinline__ float xor16(float x) { return __shfl_xor(x, 16); }
+__device__ __forceinline__ float xor32(float x) { return __shfl_xor(x, 32); }
+
+// 2^d for a whole number d, held within what fp32 can scale by.
+__device__ __forceinline__ float pow2(float d) {
+  return ldexpf(1.f, static_cast<int>(fminf(fmaxf(d, -200.f), 126.f)));
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -__builtin_inff() : __builtin_fmaf(m, 0.693147180559945309f, logf(ldexpf(l, -static_cast<int>(kUp))));
+}
+
+// One wave's state for NQ tiles of 16 rows.
+template <typename T, int D, int NQ>
+struct Wave {
+  static constexpr int NP = sizeof(T) == 4 ? 2 : 1;                  // f16 parts of a query
+  static constexpr int NW = std::is_same<T, bf16>::value ? 1 : 2;  // f16 parts of a weight
+  static constexpr int NC = D / 32;               // products of 32 elements
+  static constexpr int ND = D / 16;               // output tiles of 16 elements
+  static constexpr int NK = D >= 64 ? D / 64 : 1; // 16-byte loads of a key row per lane (8 bytes for D = 32)
+  h8 q[NQ][NP][NC];
+  f4 acc[NQ][ND];
+  float m[NQ], m2[NQ], rel[NQ], l[NQ], qs[NQ];
+  int hi[NQ], lo[NQ];  // the row sees positions lo <= p < hi
+
+  __device__ __forceinline__ void load_queries(const Args &a, int r, int kvh, int row0, int rows, int first_token,
+                                               int fresh, int length) {
+    const int lane = lane_id(), n = lane % 16, g = lane / 16;
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+      const int row = row0 + 16 * x + n;
+      const bool real = row < rows;
+      const int i = real ? row / a.group : 0, head = kvh * a.group + (real ? row % a.group : 0);
+      const T *p = static_cast<const T *>(a.q) + (first_token + i) * a.q_tok + head * a.q_head;
+      float v[NC][8];
+      float top = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int d = D >= 64 ? (c / 2) * 64 + g * 16 + (c % 2) * 8 : g * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[c][j] = real ? static_cast<float>(p[d + j]) : 0.f;
+          top = fmaxf(top, fabsf(v[c][j]));
+        }
+      }
+      top = fmaxf(top, xor16(top));
+      top = fmaxf(top, xor32(top));
+      int e = 0;
+      if (top > 0.f && top <= 3.402823466e38f) e = 9 - ilogbf(top);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float y = a.scale < 0.f ? -ldexpf(v[c][j], e) : ldexpf(v[c][j], e);  // scales in weights() are not negative
+          q[x][0][c][j] = static_cast<_Float16>(y);
+          if constexpr (NP == 2) q[x][1][c][j] = static_cast<_Float16>(y - static_cast<float>(q[x][0][c][j]));
+        }
+      qs[x] = ldexpf(fabsf(a.scale), -e);
+      hi[x] = 0;
+      lo[x] = 0;
+      if (real) {
+        hi[x] = length;
+        if (a.causal) {
+          const int at = length - fresh + i;
+          hi[x] = max(at + 1, 0);
+          if (a.window > 0) lo[x] = max(at + 1 - a.window, 0);
+        }
+      }
+      m[x] = m2[x] = kNone;
+      rel[x] = 1.f;
+      l[x] = 0.f;
+#pragma unroll
+      for (int e2 = 0; e2 < ND; ++e2) acc[x][e2] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+  }
+
+  // One tile: kr, vr the raw codes, ks/vs the scales of this lane's chunk
+  // (chunk ok: the lane's own chunk has a block), base the tile's position.
+  __device__ __forceinline__ void scores(const u4 (&kr)[4][NK], f4 (&s)[NQ][4]) const {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) s[x][t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const u4 w = kr[t][c / 2];
+        const h8 kf = (c % 2) ? f16_of_codes(w[2], w[3]) : f16_of_codes(w[0], w[1]);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) s[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[x][p][c], s[x][t], 0, 0, 0);
+      }
+    }
+  }
+
+  // Masks the scores, keeps the running maxima (m of the scores, m2 of the scores times the value scales, both in
+  // log2 and whole numbers, so every rescaling is exact), adds up l and leaves the weights times the value scales in
+  // s.  Maxima are compared per lane and joined over the lane groups only when some lane passes them by kSlack; a row
+  // follows its own scores alone.
+  __device__ __forceinline__ void weights(f4 (&s)[NQ][4], float ks, float vs, bool ok, int base) {
+    const int g = lane_id() / 16;
+    if (!ok) ks = 0.f, vs = 0.f;
+    const float ev = vs > 0.f ? static_cast<float>(__builtin_amdgcn_frexp_expf(vs)) : -__builtin_inff();
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+      float f = ks * qs[x];
+      const bool whole = base >= lo[x] && base + kTile <= hi[x] && ok;
+      if (ballot(!whole)) {
+        const int p0 = base + 16 * g;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 4 * t + i;
+            s[x][t][i] = (ok && p >= lo[x] && p < hi[x]) ? s[x][t][i] * f : -__builtin_inff();
+          }
+        f = 1.f;
+      }
+      float top = s[x][0][0];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[x][t][i]);
+      top *= f;
+      if (ballot(top > m[x] + kSlack || top + ev > m2[x] + kSlack)) {
+        float top2 = top + ev;
+        top = fmaxf(top, xor16(top));
+        top = fmaxf(top, xor32(top));
+        top2 = fmaxf(top2, xor16(top2));
+        top2 = fmaxf(top2, xor32(top2));
+        const float now = top > m[x] + kSlack ? __builtin_ceilf(top) : m[x];
+        const float now2 = top2 > m2[x] + kSlack ? __builtin_ceilf(top2) : m2[x];
+        l[x] *= pow2(m[x] - now);
+        const float by = pow2(m2[x] - now2);
+#pragma unroll
+        for (int e = 0; e < ND; ++e) acc[x][e] *= by;
+        m[x] = now;
+        m2[x] = now2;
+        rel[x] = pow2(now - now2);
+      }
+      // finite even where the best scores' values are all zero (a scale of 0) and m is far above m2: p is 0 there
+      const float off = kUp - m[x], c = fminf(vs * rel[x], 3.402823466e38f);
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x][t][i], f, off));
+          sum += p;
+          s[x][t][i] = p * c;
+        }
+      l[x] += sum;
+    }
+  }
+
+  __device__ __forceinline__ void values(const u4 (&vr)[ND], const f4 (&s)[NQ][4]) {
+    h8 p[NQ][NW][2];
+#pragma unroll
+    for (int x = 0; x < NQ; ++x)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float y = s[x][2 * u + j / 4][j % 4];
+          // the product's fp32 rounding has to happen before both parts are taken: without this the first
+          // part is rounded to f16 straight from the product, and at ties the two parts disagree
+          if constexpr (NW == 2) asm("" : "+v"(y));
+          p[x][0][u][j] = static_cast<_Float16>(y);
+          if constexpr (NW == 2) p[x][1][u][j] = static_cast<_Float16>(y - static_cast<float>(p[x][0][u][j]));
+        }
+#pragma unroll
+    for (int e = 0; e < ND; ++e)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const h8 vf = u ? f16_of_codes(vr[e][2], vr[e][3]) : f16_of_codes(vr[e][0], vr[e][1]);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int k = 0; k < NW; ++k) acc[x][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[x][k][u], acc[x][e], 0, 0, 0);
+      }
+  }
+};
+
+// The block ids of a lane: `own` for its chunk lane/16 (scales, values), `row`
+// for the key rows it loads (chunk (lane%16)/4).
+struct Ids {
+  int own, row;
+};
+
+__device__ __forceinline__ int block_of(const Args &a, const int *table, int pos) {
+  const int64_t col = pos >> a.log_b;
+  int b = -1;
+  if (col < a.cols) b = table[col];
+  return b >= 0 && b < a.num_blocks ? b : -1;
+}
+
+// A request's length, within what its table row and the launch cover.
+__device__ __forceinline__ int length_of(const Args &a, int r) {
+  const int64_t most = min(a.cols << a.log_b, static_cast<int64_t>(a.max_len));
+  return max(0, static_cast<int>(min(static_cast<int64_t>(a.lengths[r]), most)));
+}
+
+// kKeys: the four waves of a block share its rows and take its tiles in turn
+// (few rows, long histories); otherwise each wave has its own rows and all
+// walk the same tiles.
+template <typename T, int D, int NQ, bool kKeys>
+__global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
+  using W = Wave<T, D, NQ>;
+  const int lane = lane_id(), wave = threadIdx.x / kWave, n = lane % 16, g = lane / 16;
+  const int split = blockIdx.x / a.row_tiles, rt = a.row_tiles - 1 - blockIdx.x % a.row_tiles;
+  const int kvh = blockIdx.y, r = blockIdx.z;
+  const int first = a.cu[r], fresh = min(a.cu[r + 1], static_cast<int>(a.tokens)) - first;
+  const int rows = min(fresh, a.max_q) * a.group;
+  const int row0 = kKeys ? rt * 16 * NQ : (rt * kWaves + wave) * 16 * NQ;
+  const int block_row0 = kKeys ? row0 : rt * kWaves * 16 * NQ;
+  if (first < 0 || fresh <= 0 || block_row0 >= rows) return;
+  const int length = length_of(a, r);
+  const bool splits = a.part != nullptr;
+  const int64_t split_lo = static_cast<int64_t>(split) * a.chunk;
+  if (splits && split > 0 && split_lo >= length) return;  // the combine knows that this split is empty
+
+  W w;
+  w.load_queries(a, r, kvh, min(row0, rows), rows, first, fresh, length);
+  const int *table = a.table + r * a.cols;
+
+  // the tiles that any of the wave's rows sees
+  int see_lo = 0x7fffffff, see_hi = 0;
+#pragma unroll
+  for (int x = 0; x < NQ; ++x)
+    if (w.hi[x] > w.lo[x]) see_lo = min(see_lo, w.lo[x]), see_hi = max(see_hi, w.hi[x]);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    see_lo = min(see_lo, __shfl_xor(see_lo, o));
+    see_hi = max(see_hi, __shfl_xor(see_hi, o));
+  }
+  see_lo = __builtin_amdgcn_readfirstlane(see_lo);
+  see_hi = min(__builtin_amdgcn_readfirstlane(see_hi), length);
+  if (splits) {
+    see_lo = max(see_lo, static_cast<int>(min(split_lo, int64_t(0x7fffffff))));
+    see_hi = static_cast<int>(min(static_cast<int64_t>(see_hi), split_lo + a.chunk));
+  }
+  const int tile_lo = see_lo / kTile, tile_hi = see_hi > see_lo ? (see_hi + kTile - 1) / kTile : 0;
+  const int step = kKeys ? kWaves : 1;
+  for (int tile = tile_lo + (kKeys ? wave : 0); tile < tile_hi; tile += step) {
+    const int base = tile * kTile;
+    const int own = block_of(a, table, base + 16 * g);
+    const int row = block_of(a, table, base + 16 * (n / 4));
+    const bool ok = own >= 0;
+    const int in_b = (1 << a.log_b) - 1;
+    u4 kr[4][W::NK], vr[W::ND];
+    const int64_t kb = ((static_cast<int64_t>(max(row, 0)) * a.kv_heads + kvh) << a.log_b) * D;
+    const int64_t vb = ((static_cast<int64_t>(max(own, 0)) * a.kv_heads + kvh) << a.log_b) * D;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int at = (base + 16 * (n / 4) + 4 * t + n % 4) & in_b;
+      const int8_t *p = a.k + kb + static_cast<int64_t>(at) * D;
+      if constexpr (D >= 64) {
+#pragma unroll
+        for (int c = 0; c < W::NK; ++c) kr[t][c] = *reinterpret_cast<const u4 *>(p + c * 64 + g * 16);
+      } else {
+        const u2 y = *reinterpret_cast<const u2 *>(p + g * 8);
+        kr[t][0] = u4{y[0], y[1], 0u, 0u};
+      }
+    }
+    const int chunk_at = ((base + 16 * g) & in_b) >> 4;
+#pragma unroll
+    for (int e = 0; e < W::ND; ++e)
+      vr[e] = *reinterpret_cast<const u4 *>(a.v + vb + (static_cast<int64_t>(chunk_at) * D + e * 16 + n) * 16);
+    const float ks = a.ks[static_cast<int64_t>(max(own, 0)) * a.kv_heads + kvh];
+    const float vs = a.vs[static_cast<int64_t>(max(own, 0)) * a.kv_heads + kvh];
+    f4 s[NQ][4];
+    w.scores(kr, s);
+    w.weights(s, ks, vs, ok, base);
+    w.values(vr, s);
+  }
+
+  // join the lane groups' sums; then, for kKeys, the waves
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    w.l[x] += xor16(w.l[x]);
+    w.l[x] += xor32(w.l[x]);
+  }
+  __shared__ float jm[kWaves][16 * NQ], jm2[kWaves][16 * NQ], jl[kWaves][16 * NQ];
+  __shared__ float ja[kKeys ? 2 : 1][kKeys ? 16 * NQ * (D + 4) : 1];
+  if constexpr (kKeys) {
+#pragma unroll
+    for (int x = 0; x < NQ; ++x)
+      if (g == 0) jm[wave][x * 16 + n] = w.m[x], jm2[wave][x * 16 + n] = w.m2[x];
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) {
+      float top = kNone, top2 = kNone;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) top = fmaxf(top, jm[k][x * 16 + n]), top2 = fmaxf(top2, jm2[k][x * 16 + n]);
+      const float by = pow2(w.m2[x] - top2);
+      w.l[x] *= pow2(w.m[x] - top);
+      w.m[x] = top;
+      w.m2[x] = top2;
+#pragma unroll
+      for (int e = 0; e < W::ND; ++e) w.acc[x][e] *= by;
+      if (g == 0) jl[wave][x * 16 + n] = w.l[x];
+    }
+    // waves 2, 3 into 0, 1, then 1 into 0
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+      if (wave >= half && wave < 2 * half)
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int e = 0; e < W::ND; ++e)
+            *reinterpret_cast<f4 *>(&ja[wave - half][(x * 16 + n) * (D + 4) + e * 16 + 4 * g]) = w.acc[x][e];
+      __syncthreads();
+      if (wave < half)
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int e = 0; e < W::ND; ++e)
+            w.acc[x][e] += *reinterpret_cast<const f4 *>(&ja[wave][(x * 16 + n) * (D + 4) + e * 16 + 4 * g]);
+      __syncthreads();
+    }
+    if (wave > 0) return;
+#pragma unroll
+    for (int x = 0; x < NQ; ++x) w.l[x] = jl[0][x * 16 + n] + jl[1][x * 16 + n] + jl[2][x * 16 + n] + jl[3][x * 16 + n];
+  }
+
+  const int heads = a.kv_heads * a.group;
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    const int row = row0 + 16 * x + n;
+    if (row >= rows) continue;
+    const int64_t at = static_cast<int64_t>(first + row / a.group) * heads + kvh * a.group + row % a.group;
+    const float inv = w.l[x] > 0.f ? 1.f / w.l[x] : (w.l[x] == 0.f ? 0.f : w.l[x]);  // a row that sees nothing: zeros
+    const float f = inv * pow2(w.m2[x] - w.m[x]);
+    if (splits) {
+      const int64_t to = static_cast<int64_t>(split) * a.tokens * heads + at;
+      if (g == 0) a.part_ml[to] = make_float2(w.m[x], w.l[x]);
+#pragma unroll
+      for (int e = 0; e < W::ND; ++e) *reinterpret_cast<f4 *>(a.part + to * D + e * 16 + 4 * g) = w.acc[x][e] * f;
+    } else {
+      T *o = static_cast<T *>(a.out) + at * D;
+      if (g == 0 && a.lse) a.lse[at] = lse_of(w.m[x], w.l[x]);
+#pragma unroll
+      for (int e = 0; e < W::ND; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[e * 16 + 4 * g + i] = static_cast<T>(w.acc[x][e][i] * f);
+    }
+  }
+}
+
+// Joins the splits of each (token, head): one wave per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) combine_kernel(Args a, int requests) {
+  const int heads = a.kv_heads * a.group, lane = lane_id();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
+  if (row >= a.tokens * heads) return;
+  const int tok = static_cast<int>(row / heads);
+  int lo = 0, hi = requests;  // the last request that begins at or before tok
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= tok)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  if (tok < a.cu[lo] || tok >= a.cu[lo + 1]) return;
+  if (tok - a.cu[lo] >= a.max_q) return;
+  const int n = max(1, static_cast<int>((static_cast<int64_t>(length_of(a, lo)) + a.chunk - 1) / a.chunk));
+  const int64_t step = a.tokens * heads;
+  float top = kNone;
+  for (int i = lane; i < n; i += kWave) top = fmaxf(top, a.part_ml[i * step + row].x);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  constexpr int NV = (D + 63) / 64;
+  float o[NV] = {}, total = 0.f;
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = a.part_ml[i * step + row];
+    const float w = __builtin_amdgcn_exp2f(ml.x - top) * ml.y;
+    total += w;
+    if (w != 0.f)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (D >= 64 || lane < D) o[k] = __builtin_fmaf(w, a.part[(i * step + row) * D + k * 64 + lane], o[k]);
+  }
+  const float inv = total > 0.f ? 1.f / total : total;  // no split sees anything: zeros
+  T *out = static_cast<T *>(a.out) + row * D;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (D >= 64 || lane < D) out[k * 64 + lane] = static_cast<T>(o[k] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[row] = lse_of(top, total);
+}
+
+struct Plan {
+  bool keys;
+  int nq, row_tiles, splits, chunk;
+};
+
+Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t max_q, int64_t max_len) {
+  Plan p{};
+  const int64_t rows = max_q * group;
+  p.keys = rows <= 16;
+  p.nq = p.keys ? 1 : 2;
+  const int64_t per = p.keys ? 16 : 16 * p.nq * kWaves;
+  p.row_tiles = static_cast<int>((rows + per - 1) / per);
+  const int64_t blocks = requests * kv_heads * p.row_tiles;
+  const int64_t most = (max_len + 255) / 256;
+  int64_t s = blocks > 0 ? (3072 + blocks - 1) / blocks : 1;
+  if (s > most) s = most;
+  if (s < 1) s = 1;
+  int64_t chunk = (max_len + s - 1) / s;
+  chunk = (chunk + 255) / 256 * 256;
+  if (chunk < 256) chunk = 256;
+  p.splits = static_cast<int>(max_len > 0 ? (max_len + chunk - 1) / chunk : 1);
+  p.chunk = static_cast<int>(chunk);
+  return p;
+}
+
+template <typename T, int D>
+hlr_status launch(const Args &a, const Plan &p, int64_t requests, hipStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.splits * p.row_tiles), static_cast<unsigned>(a.kv_heads),
+                  static_cast<unsigned>(requests));
+  if (p.keys)
+    attention_kernel<T, D, 1, true><<<grid, kWaves * kWave, 0, stream>>>(a);
+  else
+    attention_kernel<T, D, 2, false><<<grid, kWaves * kWave, 0, stream>>>(a);
+  if (p.splits > 1) {
+    const hlr_status st = launch_status();
+    if (st != HLR_OK) return st;
+    combine_kernel<T, D><<<grid_for(a.tokens * a.kv_heads * a.group, 4), 256, 0, stream>>>(a, static_cast<int>(requests));
+  }
+  return launch_status();
+}
+
+template <typename T>
+hlr_status launch_dim(const Args &a, const Plan &p, int64_t dim, int64_t requests, hipStream_t stream) {
+  switch (dim) {
+    case 32: return launch<T, 32>(a, p, requests, stream);
+    case 64: return launch<T, 64>(a, p, requests, stream);
+    case 128: return launch<T, 128>(a, p, requests, stream);
+    default: return launch<T, 256>(a, p, requests, stream);
+  }
+}
+
+bool sizes_ok(int64_t tokens, int64_t requests, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_q,
+              int64_t max_len) {
+  return tokens >= 0 && tokens <= kMaxN && requests >= 0 && requests <= HLR_HIST_MAX_REQUESTS && kv_heads > 0 &&
+         kv_heads <= 65535 && q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads <= 65535 && max_q >= 0 &&
+         max_q <= kMaxN / q_heads && max_len >= 0 && max_len <= kMaxN - 65536 &&
+         (dim == 32 || dim == 64 || dim == 128 || dim == 256);
+}
+
+}  // namespace
+
+extern "C" size_t hist_attention_workspace_size(int64_t tokens, int64_t requests, int64_t q_heads, int64_t kv_heads,
+                                                int64_t dim, int64_t max_q, int64_t max_len) {
+  if (!sizes_ok(tokens, requests, q_heads, kv_heads, dim, max_q, max_len)) return 0;
+  const Plan p = plan(requests, kv_heads, q_heads / kv_heads, max_q, max_len);
+  if (p.splits <= 1) return 0;
+  const size_t rows = static_cast<size_t>(p.splits) * tokens * q_heads;
+  return round_up(rows * dim * 4, 256) + round_up(rows * 8, 256);
+}
+
+extern "C" hlr_status hist_attention(const void *q, int32_t type, int64_t tokens, int64_t q_heads, int64_t q_token_stride,
+                                     int64_t q_head_stride, const int8_t *k_codes, const int8_t *v_codes,
+                                     const float *k_scale, const float *v_scale, int64_t num_blocks, int64_t kv_heads,
+                                     int64_t block, int64_t dim, const int32_t *block_table, int64_t table_cols,
+                                     const int32_t *lengths, const int32_t *cu, int64_t requests, int64_t max_q,
+                                     int64_t max_len, float scale, int32_t causal, int64_t window, void *out,
+                                     float *out_lse, void *ws, size_t ws_bytes, hipStream_t stream) {
+  if (dim != 32 && dim != 64 && dim != 128 && dim != 256) return HLR_UNSUPPORTED_DIM;
+  if (!sizes_ok(tokens, requests, q_heads, kv_heads, dim, max_q, max_len) || type < 0 || type > 2 ||
+      (causal != 0 && causal != 1) || window < 0 || window > kMaxN || (window > 0 && !causal) || num_blocks < 0 ||
+      num_blocks > kMaxN || table_cols < 0 || table_cols > kMaxN / 256 || !(scale == scale))
+    return HLR_INVALID_ARG;
+  int log_b = 4;
+  while (log_b <= 8 && (int64_t(1) << log_b) != block) ++log_b;
+  if (log_b > 8) return HLR_INVALID_ARG;
+  if (tokens == 0 || requests == 0 || max_q == 0) return HLR_OK;
+  if (!q || !out || !lengths || !cu || (table_cols > 0 && !block_table) ||
+      (num_blocks > 0 && (!k_codes || !v_codes || !k_scale || !v_scale)))
+    return HLR_INVALID_ARG;
+  const int64_t unit = type == HLR_FP32 ? 4 : 8;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % unit || q_head_stride % unit || !aligned(k_codes, 16) ||
+      !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) ||
+      !aligned(lengths, 4) || !aligned(cu, 4) || !aligned(out_lse, 4))
+    return HLR_MISALIGNED;
+  const Plan p = plan(requests, kv_heads, q_heads / kv_heads, max_q, max_len);
+  Args a{};
+  a.q = q;
+  a.q_tok = q_token_stride;
+  a.q_head = q_head_stride;
+  a.k = k_codes;
+  a.v = v_codes;
+  a.ks = k_scale;
+  a.vs = v_scale;
+  a.table = block_table;
+  a.cols = num_blocks > 0 ? table_cols : 0;  // no pool: every request sees nothing
+  a.lengths = lengths;
+  a.cu = cu;
+  a.out = out;
+  a.lse = out_lse;
+  a.tokens = tokens;
+  a.num_blocks = num_blocks;
+  a.kv_heads = static_cast<int>(kv_heads);
+  a.group = static_cast<int>(q_heads / kv_heads);
+  a.log_b = log_b;
+  a.causal = causal;
+  a.window = static_cast<int>(window);
+  a.scale = scale * 1.44269504088896340736f;
+  a.chunk = p.chunk;
+  a.row_tiles = p.row_tiles;
+  a.max_q = static_cast<int>(max_q);
+  a.max_len = static_cast<int>(max_len);
+  if (p.splits > 1) {
+    const size_t need = hist_attention_workspace_size(tokens, requests, q_heads, kv_heads, dim, max_q, max_len);
+    if (!ws || ws_bytes < need) return HLR_WORKSPACE_TOO_SMALL;
+    if (!aligned(ws, 256)) return HLR_MISALIGNED;
+    Carver c(ws);
+    a.part = c.take<float>(static_cast<size_t>(p.splits) * tokens * q_heads * dim);
+    a.part_ml = c.take<float2>(static_cast<size_t>(p.splits) * tokens * q_heads);
+  }
+  if (type == HLR_FP32) return launch_dim<float>(a, p, dim, requests, stream);
+  if (type == HLR_BF16) return launch_dim<bf16>(a, p, dim, requests, stream);
+  return launch_dim<_Float16>(a, p, dim, requests, stream);
+}

@@ -562,6 +562,122 @@ hlr_status memory_layer_step(int64_t *identity, int64_t *stamps, float *values, 
                              hipEvent_t planned, hipEvent_t gather_begin, hipEvent_t gather_end,
                              hipEvent_t slot_done, int32_t halves);
 
+/* ------------------------------------------------------------------------
+ * A user's event history held in 8 bits ([DLRM] sample walk-through: each user
+ * is a sequence of events, thousands long; [ML] sec. 5: serving reads int8)
+ *
+ *  A pool of num_blocks blocks of `block` tokens (a power of two, 16 to 256)
+ *  is shared by all requests; per token `heads` key and value vectors of dim
+ *  32, 64, 128 or 256 elements (else HLR_UNSUPPORTED_DIM):
+ *    k_codes int8 [num_blocks][heads][block][dim]
+ *    v_codes int8 [num_blocks][heads][block/16][dim][16]
+ *    k_scale, v_scale fp32 [num_blocks][heads]; a value is code * scale.
+ *  Codes are 16-byte aligned.  A slot is block id * block + place in the
+ *  block (int64; -1: none).  block_table int32 [requests][table_cols] holds
+ *  each request's block ids in order of position; -1: no block.
+ *  Vectors of type HLR_FP32, HLR_BF16 or HLR_FP16 are 16-byte aligned, their
+ *  elements contiguous, and strides (in elements) multiples of 16 bytes.
+ * --------------------------------------------------------------------- */
+#define HLR_FP32 0
+#define HLR_BF16 1
+#define HLR_FP16 2
+#define HLR_HIST_MAX_REQUESTS 65535
+
+/* Block tables and slot maps from request lengths.
+ *  Request r holds cached[r] tokens and gains fresh[r] (int32; negative
+ *  counts as 0).  Its new blocks, columns ceil(cached/block) up to
+ *  ceil((cached+fresh)/block) - 1 of its row, take free_blocks[num_free] in
+ *  order, requests in order; a block beyond the list is -1, and a column
+ *  beyond table_cols is not written.
+ *  block_table          in/out; other entries are left as they are.
+ *  out_slots[max_tokens] slot of each new token, requests in order; -1 where
+ *                       its block is missing, and past the last token.
+ *  out_cu[requests+1]   first token of each request, then their number.
+ *  out_lengths[requests] cached + fresh.
+ *  out_counts[2]        int64 {blocks taken of the list, new tokens whose
+ *                       block is missing}.
+ *  max_tokens must hold the batch's new tokens: later ones get no slot and
+ *  write no block.  Sums past 2^31 - 1 in out_cu and out_lengths saturate. */
+hlr_status hist_plan(const int32_t *cached, const int32_t *fresh, int64_t requests, int32_t *block_table,
+                     int64_t table_cols, const int32_t *free_blocks, int64_t num_free, int64_t block,
+                     int64_t max_tokens, int64_t *out_slots, int32_t *out_cu, int32_t *out_lengths,
+                     int64_t *out_counts, hipStream_t stream);
+
+/* Quantises new keys and values into their slots.
+ *  k, v: token t, head h at t * token_stride + h * head_stride.  The tokens of
+ *  one block stand together and fill consecutive places (as hist_plan maps
+ *  them); places before the first of them hold earlier tokens.  Slots outside
+ *  the pool are skipped.  A block touched from two places gives unspecified
+ *  codes.
+ *  NaN counts as 0 and infinities as the largest fp32 number.  Per block and
+ *  head, in fp32, each operation rounded on its own:
+ *    s' = max(fl(amax * fl(1/127)), the old scale if the block holds earlier tokens)
+ *         (a product below 2^-126 counts as 0)
+ *    new codes  clamp(rne(fl(x * fl(1/s'))), -127, 127), 0 for s' = 0
+ *    held codes rne(fl(q * fl(s * fl(1/s')))) if s' > s, else unchanged. */
+hlr_status hist_append(int8_t *k_codes, int8_t *v_codes, float *k_scale, float *v_scale, int64_t num_blocks,
+                       int64_t heads, int64_t block, int64_t dim, const void *k, const void *v, int32_t type,
+                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                       const int64_t *slots, int64_t tokens, hipStream_t stream);
+
+/* The values that slots stand for: out_k, out_v [tokens][heads][dim] of
+ * `type`, rounded once from fl(code * scale); zeros for slots outside the pool. */
+hlr_status hist_read(const int8_t *k_codes, const int8_t *v_codes, const float *k_scale, const float *v_scale,
+                     int64_t num_blocks, int64_t heads, int64_t block, int64_t dim, const int64_t *slots,
+                     int64_t tokens, void *out_k, void *out_v, int32_t type, hipStream_t stream);
+
+/* Attention of queries over the cache: out = softmax(scale q K^T) V.
+ *  q[tokens][q_heads][dim] by strides; request r's queries are tokens
+ *  cu[r] .. cu[r+1]-1 (int32, as hist_plan gives them), at most max_q of them;
+ *  its history is the first lengths[r] positions of its table row, at most
+ *  max_len.  q_heads is a multiple of kv_heads: query head h reads key head
+ *  h / (q_heads / kv_heads).
+ *  causal 1: the queries are the history's newest events; query i of n sees
+ *    positions up to length - n + i, and with window > 0 only the last
+ *    `window` of those.  causal 0: every query sees the whole history.
+ *  Positions without a block are not seen.  A query that sees nothing gets
+ *  zeros, and -inf for its lse.
+ *  out[tokens][q_heads][dim] of q's type; out_lse[tokens][q_heads] fp32,
+ *  nullable: the natural logarithm of the sum of exp(scale q k).  Tokens of no
+ *  request are not written.
+ *  Scores, softmax statistics and sums are fp32; the softmax weights are
+ *  rounded to 11 bits before the product with the values for HLR_BF16, and to
+ *  22 bits for the other types.
+ *  Workspace: hist_attention_workspace_size(...) bytes. */
+size_t hist_attention_workspace_size(int64_t tokens, int64_t requests, int64_t q_heads, int64_t kv_heads, int64_t dim,
+                                     int64_t max_q, int64_t max_len);
+hlr_status hist_attention(const void *q, int32_t type, int64_t tokens, int64_t q_heads, int64_t q_token_stride,
+                          int64_t q_head_stride, const int8_t *k_codes, const int8_t *v_codes, const float *k_scale,
+                          const float *v_scale, int64_t num_blocks, int64_t kv_heads, int64_t block, int64_t dim,
+                          const int32_t *block_table, int64_t table_cols, const int32_t *lengths, const int32_t *cu,
+                          int64_t requests, int64_t max_q, int64_t max_len, float scale, int32_t causal,
+                          int64_t window, void *out, float *out_lse, void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Sampling of one item per row of scores ([ML] sec. 1: each request has about a
+ * thousand scored candidates), from given random numbers
+ *  scores[rows][items] of `type`, rows `stride` elements apart; NaN and -inf
+ *  are items that can't be drawn, +inf counts as the largest number.
+ *  noise[rows][items] fp32, positive, distributed as Exp(1).
+ *  Per row (arrays of `rows`, each nullable): temperature (default 1; not above 0:
+ *  the best item), top_k (int32; not above 0: no limit), top_p (default: no
+ *  limit), min_p (default 0).
+ *  z = fl(x / temperature); items rank by z descending, then by index.  Kept
+ *  are the first top_k; of those, the items before which less than top_p
+ *  of their mass lies (mass: exp(z - max z)); of those, the ones with
+ *  exp(z - max z) >= min_p; and always the first.  Drawn is the kept item with
+ *  the largest z - log(noise), equal ones by rank.
+ *  out_index[rows] int64; -1 if no item can be drawn.  out_logprob[rows]: the
+ *  drawn item's z - log(sum of exp z) over all items before the filters (for
+ *  temperature 0 that of temperature 1); -inf with index -1.
+ *  items at most HLR_SAMPLE_MAX_ITEMS.
+ * --------------------------------------------------------------------- */
+#define HLR_SAMPLE_MAX_ITEMS (1 << 27)
+hlr_status sample_scores(const void *scores, int32_t type, int64_t rows, int64_t items, int64_t stride,
+                         const float *noise, int64_t noise_stride, const float *temperature, const int32_t *top_k,
+                         const float *top_p, const float *min_p, int64_t *out_index, float *out_logprob,
+                         hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
