@@ -122,9 +122,17 @@ struct Wave {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int d = D >= 64 ? (c / 2) * 64 + g * 16 + (c % 2) * 8 : g * 8;
+        // rows past the end read a real row's elements and drop them
+        T y[8];
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<u4 *>(y) = *reinterpret_cast<const u4 *>(p + d);
+          *reinterpret_cast<u4 *>(y + 4) = *reinterpret_cast<const u4 *>(p + d + 4);
+        } else {
+          *reinterpret_cast<u4 *>(y) = *reinterpret_cast<const u4 *>(p + d);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[c][j] = real ? static_cast<float>(p[d + j]) : 0.f;
+          v[c][j] = real ? static_cast<float>(y[j]) : 0.f;
           top = fmaxf(top, fabsf(v[c][j]));
         }
       }
@@ -279,6 +287,45 @@ __device__ __forceinline__ int block_of(const Args &a, const int *table, int pos
   return b >= 0 && b < a.num_blocks ? b : -1;
 }
 
+__device__ __forceinline__ Ids ids_of(const Args &a, const int *table, int tile) {
+  const int lane = lane_id(), base = tile * kTile;
+  return Ids{block_of(a, table, base + 16 * (lane / 16)), block_of(a, table, base + 16 * (lane % 16 / 4))};
+}
+
+// The raw codes of a tile's keys: row token(t, m) of the A operand, 16 bytes
+// of 64 (or 8 of 32) elements per lane.  Lanes without a block read block 0.
+template <int D, int NK>
+__device__ __forceinline__ void load_keys(const Args &a, Ids id, int kvh, int tile, u4 (&kr)[4][NK]) {
+  const int lane = lane_id(), n = lane % 16, g = lane / 16;
+  const int at = (tile * kTile + 16 * (n / 4) + n % 4) & ((1 << a.log_b) - 1);
+  const int8_t *p =
+      a.k + (((static_cast<int64_t>(max(id.row, 0)) * a.kv_heads + kvh) << a.log_b) + at) * D + g * (D >= 64 ? 16 : 8);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if constexpr (D >= 64) {
+#pragma unroll
+      for (int c = 0; c < NK; ++c) kr[t][c] = *reinterpret_cast<const u4 *>(p + t * 4 * D + c * 64);
+    } else {
+      const u2 y = *reinterpret_cast<const u2 *>(p + t * 4 * D);
+      kr[t][0] = u4{y[0], y[1], 0u, 0u};
+    }
+  }
+}
+
+// The raw codes of a tile's values (16 tokens of one element per load) and
+// the scales of this lane's chunk.
+template <int D, int ND>
+__device__ __forceinline__ void load_values(const Args &a, Ids id, int kvh, int tile, u4 (&vr)[ND], float &ks, float &vs) {
+  const int lane = lane_id(), n = lane % 16, g = lane / 16;
+  const int chunk = ((tile * kTile + 16 * g) & ((1 << a.log_b) - 1)) >> 4;
+  const int64_t bh = static_cast<int64_t>(max(id.own, 0)) * a.kv_heads + kvh;
+  const int8_t *p = a.v + (((bh << (a.log_b - 4)) + chunk) * D + n) * 16;
+#pragma unroll
+  for (int e = 0; e < ND; ++e) vr[e] = *reinterpret_cast<const u4 *>(p + e * 256);
+  ks = a.ks[bh];
+  vs = a.vs[bh];
+}
+
 // A request's length, within what its table row and the launch cover.
 __device__ __forceinline__ int length_of(const Args &a, int r) {
   const int64_t most = min(a.cols << a.log_b, static_cast<int64_t>(a.max_len));
@@ -325,38 +372,32 @@ __global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
     see_hi = static_cast<int>(min(static_cast<int64_t>(see_hi), split_lo + a.chunk));
   }
   const int tile_lo = see_lo / kTile, tile_hi = see_hi > see_lo ? (see_hi + kTile - 1) / kTile : 0;
+  // Loads run ahead of the products: a tile's keys are fetched while the tile before it is weighted, its values and
+  // scales while the tile before it ends, its block ids one tile earlier still.
   const int step = kKeys ? kWaves : 1;
-  for (int tile = tile_lo + (kKeys ? wave : 0); tile < tile_hi; tile += step) {
-    const int base = tile * kTile;
-    const int own = block_of(a, table, base + 16 * g);
-    const int row = block_of(a, table, base + 16 * (n / 4));
-    const bool ok = own >= 0;
-    const int in_b = (1 << a.log_b) - 1;
+  int tile = tile_lo + (kKeys ? wave : 0);
+  if (tile < tile_hi) {
+    Ids now = ids_of(a, table, tile), next = tile + step < tile_hi ? ids_of(a, table, tile + step) : Ids{-1, -1};
     u4 kr[4][W::NK], vr[W::ND];
-    const int64_t kb = ((static_cast<int64_t>(max(row, 0)) * a.kv_heads + kvh) << a.log_b) * D;
-    const int64_t vb = ((static_cast<int64_t>(max(own, 0)) * a.kv_heads + kvh) << a.log_b) * D;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int at = (base + 16 * (n / 4) + 4 * t + n % 4) & in_b;
-      const int8_t *p = a.k + kb + static_cast<int64_t>(at) * D;
-      if constexpr (D >= 64) {
-#pragma unroll
-        for (int c = 0; c < W::NK; ++c) kr[t][c] = *reinterpret_cast<const u4 *>(p + c * 64 + g * 16);
-      } else {
-        const u2 y = *reinterpret_cast<const u2 *>(p + g * 8);
-        kr[t][0] = u4{y[0], y[1], 0u, 0u};
+    float ks, vs;
+    load_keys<D>(a, now, kvh, tile, kr);
+    load_values<D>(a, now, kvh, tile, vr, ks, vs);
+    while (true) {
+      const int base = tile * kTile;
+      const bool more = tile + step < tile_hi, ok = now.own >= 0;
+      f4 s[NQ][4];
+      w.scores(kr, s);
+      now = next;
+      if (more) {
+        load_keys<D>(a, next, kvh, tile + step, kr);
+        if (tile + 2 * step < tile_hi) next = ids_of(a, table, tile + 2 * step);
       }
+      w.weights(s, ks, vs, ok, base);
+      w.values(vr, s);
+      if (!more) break;
+      tile += step;
+      load_values<D>(a, now, kvh, tile, vr, ks, vs);
     }
-    const int chunk_at = ((base + 16 * g) & in_b) >> 4;
-#pragma unroll
-    for (int e = 0; e < W::ND; ++e)
-      vr[e] = *reinterpret_cast<const u4 *>(a.v + vb + (static_cast<int64_t>(chunk_at) * D + e * 16 + n) * 16);
-    const float ks = a.ks[static_cast<int64_t>(max(own, 0)) * a.kv_heads + kvh];
-    const float vs = a.vs[static_cast<int64_t>(max(own, 0)) * a.kv_heads + kvh];
-    f4 s[NQ][4];
-    w.scores(kr, s);
-    w.weights(s, ks, vs, ok, base);
-    w.values(vr, s);
   }
 
   // join the lane groups' sums; then, for kKeys, the waves
@@ -432,12 +473,14 @@ __global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
   }
 }
 
-// Joins the splits of each (token, head): one wave per row.
+// Joins the splits of each (token, head), one block per row: the threads' first
+// pass finds the largest maximum, then each of 1024 / D groups of D / 4
+// threads adds every such group's share of the splits, four elements a thread.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) combine_kernel(Args a, int requests) {
-  const int heads = a.kv_heads * a.group, lane = lane_id();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / kWave;
-  if (row >= a.tokens * heads) return;
+  constexpr int kPer = D / 4, kGroups = 256 / kPer;
+  const int heads = a.kv_heads * a.group, tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
   const int tok = static_cast<int>(row / heads);
   int lo = 0, hi = requests;  // the last request that begins at or before tok
   while (hi - lo > 1) {
@@ -451,28 +494,51 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a, int requests) {
   if (tok - a.cu[lo] >= a.max_q) return;
   const int n = max(1, static_cast<int>((static_cast<int64_t>(length_of(a, lo)) + a.chunk - 1) / a.chunk));
   const int64_t step = a.tokens * heads;
+  __shared__ float wave_top[4], weight[256];
+  __shared__ f4 joined[kGroups][kPer];
   float top = kNone;
-  for (int i = lane; i < n; i += kWave) top = fmaxf(top, a.part_ml[i * step + row].x);
+  for (int i = tid; i < n; i += 256) top = fmaxf(top, a.part_ml[i * step + row].x);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  constexpr int NV = (D + 63) / 64;
-  float o[NV] = {}, total = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = a.part_ml[i * step + row];
-    const float w = __builtin_amdgcn_exp2f(ml.x - top) * ml.y;
-    total += w;
-    if (w != 0.f)
+  if (lane_id() == 0) wave_top[tid / kWave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+  const int mine = tid / kPer, at = tid % kPer;
+  const f4 *part = reinterpret_cast<const f4 *>(a.part) + row * kPer + at;
+  f4 o = {0.f, 0.f, 0.f, 0.f};
+  float total = 0.f;
+  for (int base = 0; base < n; base += 256) {
+    const int held = min(n - base, 256);
+    if (base > 0) __syncthreads();
+    if (tid < held) {
+      const float2 ml = a.part_ml[(base + tid) * step + row];
+      weight[tid] = __builtin_amdgcn_exp2f(ml.x - top) * ml.y;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int i = mine; i < held; i += kGroups) {
+      const float w = weight[i];
+      const f4 y = part[(base + i) * step * kPer];
+      total += w;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (D >= 64 || lane < D) o[k] = __builtin_fmaf(w, a.part[(i * step + row) * D + k * 64 + lane], o[k]);
+      for (int j = 0; j < 4; ++j) o[j] = __builtin_fmaf(w, y[j], o[j]);
+    }
+  }
+  __shared__ float totals[kGroups];
+  joined[mine][at] = o;
+  if (at == 0) totals[mine] = total;
+  __syncthreads();
+  if (mine > 0) return;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) {
+    o += joined[k][at];
+    total += totals[k];
   }
   const float inv = total > 0.f ? 1.f / total : total;  // no split sees anything: zeros
-  T *out = static_cast<T *>(a.out) + row * D;
+  T *out = static_cast<T *>(a.out) + row * D + at * 4;
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if (D >= 64 || lane < D) out[k * 64 + lane] = static_cast<T>(o[k] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[row] = lse_of(top, total);
+  for (int j = 0; j < 4; ++j) out[j] = static_cast<T>(o[j] * inv);
+  if (at == 0 && a.lse) a.lse[row] = lse_of(top, total);
 }
 
 struct Plan {
@@ -489,7 +555,11 @@ Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t max_q, int6
   p.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t blocks = requests * kv_heads * p.row_tiles;
   const int64_t most = (max_len + 255) / 256;
-  int64_t s = blocks > 0 ? (3072 + blocks - 1) / blocks : 1;
+  // With keys shared by a block's waves: enough blocks that ragged lengths even out, but none for fewer than 256
+  // tokens.  With rows of their own: only where the rows leave most of the GPU idle.
+  const int64_t want = p.keys ? 4096 : 512;
+  int64_t s = blocks > 0 ? (want + blocks - 1) / blocks : 1;
+  if (!p.keys && blocks > 256) s = 1;
   if (s > most) s = most;
   if (s < 1) s = 1;
   int64_t chunk = (max_len + s - 1) / s;
@@ -511,7 +581,7 @@ hlr_status launch(const Args &a, const Plan &p, int64_t requests, hipStream_t st
   if (p.splits > 1) {
     const hlr_status st = launch_status();
     if (st != HLR_OK) return st;
-    combine_kernel<T, D><<<grid_for(a.tokens * a.kv_heads * a.group, 4), 256, 0, stream>>>(a, static_cast<int>(requests));
+    combine_kernel<T, D><<<grid_for(a.tokens * a.kv_heads * a.group, 1), 256, 0, stream>>>(a, static_cast<int>(requests));
   }
   return launch_status();
 }
