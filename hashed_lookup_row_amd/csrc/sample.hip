@@ -1,40 +1,59 @@
 // Sampling one item per row of scores with temperature, top-k, top-p and
 // min-p, from given random numbers.
 //
-// z = x / temperature; items rank by (z descending, index ascending); the
-// filters keep a prefix of that order:
+// With f = log2(e) / temperature, w = 2^((x - max x) f); items rank by (x
+// descending, index ascending); the filters keep a prefix of that order:
 //   top-k  the first k
-//   top-p  item i while the mass of the items before it is below top_p times
-//          the mass of the first k    (mass: w = exp(z - max z))
+//   top-p  item i while the mass (sum of w) of the items before it is below
+//          top_p times the mass of the first k
 //   min-p  w >= min_p
 // and always the first item.  Of the kept items the one with the largest
-// z - log(noise) is drawn (noise ~ Exp(1): an exponential race, so item i wins
-// with probability w_i over the kept mass).
+// x / temperature - log(noise) is drawn (noise ~ Exp(1): an exponential race, so
+// item i wins with probability w_i over the kept mass).  Only the kept items'
+// noise is read.
 //
-// A prefix is a threshold key and a number of items kept of those equal to it
-// (in index order), so nothing is sorted: a row is read once into registers
-// (rows that do not fit are read again for each pass), and a radix selection over the
-// order-preserving integer of z finds the key by counts (top-k) or by masses
-// (top-p).  Masses are summed as whole numbers of 2^-36, so the result does
-// not depend on the order of the additions.  Only the kept items' noise is
-// read.  One block per row.
+// One block per row:
+//   1. the maximum, each thread's own maximum, and the sum of w (against a
+//      running maximum per thread);
+//   2. a bound below which no kept item lies: min-p's own, and the r-th largest
+//      of the threads' maxima (at least r items reach it), r = k, or half
+//      the threads where top-k is off.  The items that reach it, about as many
+//      as r, go to a list in LDS;
+//   3. a list of at most one item per thread is sorted by (x, index), and rank,
+//      mass before and the race follow per thread.
+// Where the list doesn't hold the prefix or is too long (a flat row with a
+// large top-p, many equal scores), the prefix is found as a threshold over the
+// list or the row itself: for top-p alone by linear bins of log2 w
+// (select_share), else by a radix selection (select_prefix), by counts
+// for top-k, by masses in whole numbers of 2^-36 for top-p, so that no result hangs
+// on the order of atomics.
 #include "hlr_common.hpp"
 #include "hist_common.hpp"
+
+#include <type_traits>
 
 namespace {
 using namespace hlr;
 
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
 constexpr float kMass = 68719476736.f;  // 2^36
 constexpr int kBins = 2048;
+constexpr int kList = 4096;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kMost = 3.402823466e38f;
 
-__device__ __forceinline__ uint32_t key_of(float z) {
-  const uint32_t u = __builtin_bit_cast(uint32_t, z + 0.f);  // -0 counts as 0
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f);  // -0 counts as 0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __builtin_bit_cast(float, (k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
+// NaN counts as -inf, +inf as the largest number.
+__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, -__builtin_inff()), kMost); }
+// The key of an item: 0 for those that can't be drawn.
+__device__ __forceinline__ uint32_t item_key(float x) { return x > -__builtin_inff() ? key_of(x) : 0u; }
 
 struct SampleArgs {
   const void *scores;
@@ -49,311 +68,735 @@ struct SampleArgs {
   float *logprob;
 };
 
-template <typename T, int NT, int E>
-struct Row {
-  static constexpr int kWavesN = NT / kWave;
-  const T *x;
-  int items;
-  float temperature;
-  bool divide;
-  uint32_t held[E > 0 ? E : 1];
-
-  // key of item i: 0 for items that can't be drawn (NaN, -inf)
-  __device__ __forceinline__ uint32_t make(int i) const {
-    float z = static_cast<float>(x[i]);
-    if (divide) z = z / temperature;
-    return z > -__builtin_inff() ? key_of(fminf(z, 3.402823466e38f)) : 0u;
+// What a row's items are measured against.
+struct Scale {
+  float top, f;  // the largest x; log2(e) / temperature
+  __device__ __forceinline__ float weight(float x) const { return __builtin_amdgcn_exp2f((x - top) * f); }
+  __device__ __forceinline__ uint64_t mass(float x) const {
+    return static_cast<uint64_t>(__builtin_rintf(weight(x) * kMass));
   }
-  __device__ __forceinline__ void load() {
-    if constexpr (E > 0) {
+};
+
+// A granule: 16 bytes of scores, of any alignment.
+template <typename T>
+struct Granule {
+  static constexpr int N = 16 / sizeof(T);
+  u4 raw;
+  static constexpr uint64_t kInf = sizeof(T) == 4                ? 0xff800000ff800000ull
+                                   : std::is_same<T, bf16>::value ? 0xff80ff80ff80ff80ull
+                                                                  : 0xfc00fc00fc00fc00ull;  // -inf, repeated
+  // A granule that lies in the row; -inf for others.
+  __device__ __forceinline__ void load(const T *x, int first, int items) {
+    const uint64_t none[2] = {kInf, kInf};
+    __builtin_memcpy(&raw, none, 16);
+    if (first <= items - N) __builtin_memcpy(&raw, x + first, 16);
+  }
+  // The granule that the row ends in: its last 16 bytes moved down, -inf past them.
+  __device__ __forceinline__ void load_end(const T *x, int first, int items) {
+    uint64_t w[2] = {kInf, kInf};
+    if (first < items) {
+      const int bits = (first + N - items) * static_cast<int>(8 * sizeof(T));
+      if (items >= N) {
+        __builtin_memcpy(w, x + items - N, 16);
+      } else {
+        T t[N];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = e * NT + threadIdx.x;
-        held[e] = i < items ? make(i) : 0u;
+        for (int j = 0; j < N; ++j) t[j] = j < N - items ? static_cast<T>(0.f) : x[j - (N - items)];
+        __builtin_memcpy(w, t, 16);
+      }
+      if (bits < 64) {
+        w[0] = w[0] >> bits | w[1] << (64 - bits);
+        w[1] = w[1] >> bits | kInf << (64 - bits);
+      } else {
+        w[0] = bits == 64 ? w[1] : w[1] >> (bits - 64) | kInf << (128 - bits);
+        w[1] = kInf;
       }
     }
+    __builtin_memcpy(&raw, w, 16);
   }
+  __device__ __forceinline__ float at(int j) const {
+    T t[N];
+    __builtin_memcpy(t, &raw, 16);
+    return clean(static_cast<float>(t[j]));
+  }
+};
+
+// The whole row, from memory.
+template <typename T, int NT>
+struct RowItems {
+  const T *x;
+  int items;
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    if constexpr (E > 0) {
+    using G = Granule<T>;
+    for (int first = threadIdx.x * G::N; first < items; first += NT * G::N) {
+      G g;
+      if (first <= items - G::N)
+        g.load(x, first, items);
+      else
+        g.load_end(x, first, items);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f(e * NT + threadIdx.x, held[e]);
-    } else {
-      for (int i = threadIdx.x; i < items; i += NT) f(i, make(i));
+      for (int j = 0; j < G::N; ++j) f(first + j, item_key(g.at(j)));
     }
   }
 };
 
+// The list in LDS: key and complemented index.
 template <int NT>
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *tmp) {
+struct ListItems {
+  const uint64_t *list;
+  int n;
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const uint64_t c = list[i];
+      f(static_cast<int>(~static_cast<uint32_t>(c)), static_cast<uint32_t>(c >> 32));
+    }
+  }
+};
+
+// Items as another function enumerates them.
+template <typename Each>
+struct Through {
+  const Each &by;
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    by(f);
+  }
+};
+
+// ---- reductions over a block; tmp holds 17 entries
+template <int NT>
+__device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t *tmp) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o)));
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint64_t y = __shfl_xor(v, o);
+    v = y > v ? y : v;
+  }
+  if (NT == kWave) return v;
+  __syncthreads();
   if (lane_id() == 0) tmp[threadIdx.x / kWave] = v;
   __syncthreads();
   v = tmp[0];
 #pragma unroll
-  for (int w = 1; w < NT / kWave; ++w) v = max(v, tmp[w]);
-  __syncthreads();
+  for (int w = 1; w < NT / kWave; ++w) v = tmp[w] > v ? tmp[w] : v;
   return v;
 }
 
 template <int NT>
-__device__ __forceinline__ float block_sum(float v, uint32_t *tmp) {
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *tmp) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if (lane_id() == 0) tmp[threadIdx.x / kWave] = __builtin_bit_cast(uint32_t, v);
+  if (NT == kWave) return v;
   __syncthreads();
-  v = 0.f;
-#pragma unroll
-  for (int w = 0; w < NT / kWave; ++w) v += __builtin_bit_cast(float, tmp[w]);
-  __syncthreads();
-  return v;
-}
-
-template <int NT>
-__device__ __forceinline__ uint64_t block_sum64(uint64_t v, uint64_t *tmp) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
   if (lane_id() == 0) tmp[threadIdx.x / kWave] = v;
   __syncthreads();
   v = 0;
 #pragma unroll
   for (int w = 0; w < NT / kWave; ++w) v += tmp[w];
-  __syncthreads();
   return v;
 }
 
-__device__ __forceinline__ float weight(uint32_t key, float top) {
-  return __builtin_amdgcn_exp2f((of_key(key) - top) * kLog2e);
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, uint64_t *tmp) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  if (NT == kWave) return v;
+  float *t = reinterpret_cast<float *>(tmp);
+  __syncthreads();
+  if (lane_id() == 0) t[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < NT / kWave; ++w) v += t[w];
+  return v;
 }
-__device__ __forceinline__ uint64_t mass_of(float w) { return static_cast<uint64_t>(__builtin_rintf(w * kMass)); }
 
-// Finds, among the items with key >= floor, the key t at which the total
-// of the items above it is still below `target` while that of the items at or
-// above it reaches it (or the lowest key there is); `above` receives the total above t.
-// Totals are counts (kMassed false) or masses.
-template <bool kMassed, typename R, int NT>
-__device__ uint32_t select_key(const R &row, uint32_t floor, float top, uint64_t target, uint64_t *bins, uint64_t *tmp,
-                               uint64_t &above) {
+// The value of lane ^ J, without LDS.
+template <int J>
+__device__ __forceinline__ uint32_t from_lane_xor(uint32_t v) {
+  const int x = static_cast<int>(v);
+  if constexpr (J == 1) {
+    return __builtin_amdgcn_mov_dpp(x, 0xB1, 0xf, 0xf, true);  // quad_perm 1 0 3 2
+  } else if constexpr (J == 2) {
+    return __builtin_amdgcn_mov_dpp(x, 0x4E, 0xf, 0xf, true);  // quad_perm 2 3 0 1
+  } else if constexpr (J == 4) {  // row_half_mirror (lane ^ 7), then quad_perm 3 2 1 0 (lane ^ 3)
+    return __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(x, 0x141, 0xf, 0xf, true), 0x1B, 0xf, 0xf, true);
+  } else if constexpr (J == 8) {
+    return __builtin_amdgcn_mov_dpp(x, 0x128, 0xf, 0xf, true);  // row_ror 8
+  } else if constexpr (J == 16) {
+    const auto y = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (lane_id() & 16) ? y[0] : y[1];
+  } else {
+    const auto y = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (lane_id() & 32) ? y[0] : y[1];
+  }
+}
+template <int J>
+__device__ __forceinline__ uint64_t from_lane_xor(uint64_t v) {
+  return static_cast<uint64_t>(from_lane_xor<J>(static_cast<uint32_t>(v >> 32))) << 32 |
+         from_lane_xor<J>(static_cast<uint32_t>(v));
+}
+
+// One step of the bitonic network: the larger of v and y goes to the thread
+// whose bits J and K are alike.
+template <int K, int J, typename U>
+__device__ __forceinline__ U keep(U v, U y) {
+  const bool larger = ((threadIdx.x & J) == 0) == ((threadIdx.x & K) == 0);
+  return (v > y) == larger ? v : y;
+}
+template <int K, int J, typename U>
+__device__ __forceinline__ U merge_in_wave(U v) {
+  v = keep<K, J>(v, from_lane_xor<J>(v));
+  if constexpr (J > 1) v = merge_in_wave<K, J / 2>(v);
+  return v;
+}
+template <int NT, int K, int J, typename U>
+__device__ __forceinline__ U merge(U v, U *buf, int &turn) {
+  if constexpr (J >= kWave) {
+    U *b = buf + (turn ^= 1) * NT;  // the buffers take turns, so one barrier per step is enough
+    b[threadIdx.x] = v;
+    __syncthreads();
+    v = keep<K, J>(v, b[threadIdx.x ^ J]);
+    return merge<NT, K, J / 2>(v, buf, turn);
+  } else {
+    return merge_in_wave<K, J>(v);
+  }
+}
+template <int NT, int K, typename U>
+__device__ __forceinline__ U sort_from(U v, int size, U *buf, int &turn) {
+  if (K > size) return v;
+  v = merge<NT, K, K / 2>(v, buf, turn);
+  if constexpr (K < NT) v = sort_from<NT, 2 * K>(v, size, buf, turn);
+  return v;
+}
+// Sorts one value per thread in descending order by the bitonic network, in
+// runs of `size` (a power of two from 64); buf holds 2 NT.
+template <int NT, typename U>
+__device__ __forceinline__ U block_sort(U v, int size, U *buf) {
+  int turn = 0;
+  __syncthreads();
+  return sort_from<NT, 2>(v, size, buf, turn);
+}
+
+// Finds, among the items with key >= floor, the lowest key t above which the
+// total is still below `target`; `above` receives the total above t.  Totals are
+// counts (kMassed false) or masses.
+template <bool kMassed, int NT, typename Items>
+__device__ uint32_t select_key(const Items &items, uint32_t floor, Scale sc, uint64_t target, uint64_t *bins,
+                               uint64_t *tmp, uint64_t &above) {
   uint32_t prefix = 0, mask = 0;
   above = 0;
   const int shifts[3] = {21, 10, 0}, widths[3] = {11, 11, 10};
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = shifts[pass];
     const uint32_t field = (1u << widths[pass]) - 1u;
+    __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += NT) bins[i] = 0;
     __syncthreads();
-    row.each([&](int, uint32_t k) {
+    items.each([&](int, uint32_t k) {
       if (k != 0 && k >= floor && (k & mask) == prefix)
         atomicAdd(reinterpret_cast<unsigned long long *>(&bins[(k >> shift) & field]),
-                  static_cast<unsigned long long>(kMassed ? mass_of(weight(k, top)) : 1));
+                  static_cast<unsigned long long>(kMassed ? sc.mass(of_key(k)) : 1));
     });
     __syncthreads();
-    // the lowest bin (bins descend in rank) whose total above is below the target and that is not empty
-    constexpr int per = kBins / NT > 0 ? kBins / NT : 1;
+    // bins descend in rank; the last non-empty one whose total above is below the target
+    constexpr int per = kBins / NT;
     uint64_t mine = 0;
     const int b0 = kBins - 1 - threadIdx.x * per;
 #pragma unroll
-    for (int j = 0; j < per; ++j)
-      if (b0 - j >= 0) mine += bins[b0 - j];
+    for (int j = 0; j < per; ++j) mine += bins[b0 - j];
     uint64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
       const uint64_t y = __shfl_up(incl, o);
       if (lane_id() >= o) incl += y;
     }
+    __syncthreads();
     if (lane_id() == kWave - 1) tmp[threadIdx.x / kWave] = incl;
-    if (threadIdx.x == 0) tmp[16] = ~0ull;
     __syncthreads();
-    uint64_t before = above + incl - mine;
-    for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) before += tmp[w];
-    // candidates: non-empty bins with total above < target; the lowest wins, i.e. the largest descending position
+    uint64_t run = above + incl - mine;
+    for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
     int best = -1;
-    uint64_t best_above = 0, run = before;
+    uint64_t best_above = 0;
 #pragma unroll
-    for (int j = 0; j < per; ++j)
-      if (b0 - j >= 0) {
-        const uint64_t c = bins[b0 - j];
-        if (c != 0 && run < target) best = kBins - 1 - (b0 - j), best_above = run;
-        run += c;
-      }
-    __syncthreads();
-    uint32_t *t32 = reinterpret_cast<uint32_t *>(tmp);
-    const uint32_t win = block_max<NT>(static_cast<uint32_t>(best + 1), t32);
-    if (best >= 0 && static_cast<uint32_t>(best + 1) == win) tmp[16] = best_above;
-    __syncthreads();
+    for (int j = 0; j < per; ++j) {
+      const uint64_t c = bins[b0 - j];
+      if (c != 0 && run < target) best = kBins - 1 - (b0 - j), best_above = run;
+      run += c;
+    }
+    const uint32_t win = static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(best + 1), tmp));
     if (win == 0) return 0;  // nothing there
-    above = tmp[16];
-    const uint32_t bin = kBins - win;
-    prefix |= bin << shift;
-    mask |= field << shift;
+    if (static_cast<uint32_t>(best + 1) == win) tmp[16] = best_above;
     __syncthreads();
+    above = tmp[16];
+    prefix |= (kBins - win) << shift;
+    mask |= field << shift;
   }
   return prefix;
 }
 
-template <typename T, int NT, int E>
-__global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
-  using R = Row<T, NT, E>;
-  __shared__ uint64_t bins[kBins];
-  __shared__ uint64_t tmp64[17];
-  __shared__ uint32_t cut;
-  __shared__ uint64_t race_key[NT / kWave];
-  __shared__ uint32_t race_z[NT / kWave];
-  uint32_t *tmp = reinterpret_cast<uint32_t *>(tmp64);
-  const int64_t r = blockIdx.x;
-  const int items = static_cast<int>(a.items);
-  R row;
-  row.x = static_cast<const T *>(a.scores) + r * a.stride;
-  row.items = items;
-  row.temperature = a.temperature ? a.temperature[r] : 1.f;
-  const bool race = row.temperature > 0.f;
-  row.divide = race && row.temperature != 1.f;
-  row.load();
+struct Filters {
+  int k;         // 0: none
+  float p, min;  // 1, 0: none
+};
 
-  uint32_t best = 0;
-  row.each([&](int, uint32_t k) { best = max(best, k); });
-  best = block_max<NT>(best, tmp);
+struct Drawn {
+  uint32_t key, index;
+};
+
+// The race, for items in any order: by score, then by rank.
+struct Race {
+  float score = -__builtin_inff();
+  uint32_t key = 0, index = 0;  // key 0: nobody yet
+  __device__ __forceinline__ void enter(float s, uint32_t k, uint32_t i) {
+    if (s == s && (key == 0 || s > score || (s == score && (k > key || (k == key && i < index))))) score = s, key = k, index = i;
+  }
+  __device__ __forceinline__ void meet(const Race &y) {
+    if (y.key != 0) enter(y.score, y.key, y.index);
+  }
+  template <int NT>
+  __device__ __forceinline__ void block_join(uint64_t *buf) {  // 2 * NT / 64 entries
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      Race y;
+      y.score = __shfl_xor(score, o);
+      y.key = static_cast<uint32_t>(__shfl_xor(static_cast<int>(key), o));
+      y.index = static_cast<uint32_t>(__shfl_xor(static_cast<int>(index), o));
+      meet(y);
+    }
+    if (NT == kWave) return;
+    __syncthreads();
+    if (lane_id() == 0) {
+      buf[threadIdx.x / kWave] = static_cast<uint64_t>(key) << 32 | index;
+      buf[NT / kWave + threadIdx.x / kWave] = __builtin_bit_cast(uint32_t, score);
+    }
+    __syncthreads();
+    for (int w = 0; w < NT / kWave; ++w) {
+      Race y;
+      y.score = __builtin_bit_cast(float, static_cast<uint32_t>(buf[NT / kWave + w]));
+      y.key = static_cast<uint32_t>(buf[w] >> 32);
+      y.index = static_cast<uint32_t>(buf[w]);
+      meet(y);
+    }
+  }
+};
+
+// The kept prefix as a threshold, over items in any order; total: the mass
+// of all items where top-k is off.
+template <int NT, typename Items>
+__device__ Drawn select_prefix(const Items &items, Scale sc, Filters flt, float divisor, const float *noise,
+                               uint64_t total, uint64_t *bins, uint64_t *tmp) {
+  uint32_t edge = 1;  // kept: keys above `edge`, and of those equal to it the first `ties` by index
+  uint64_t ties = ~0ull, above;
+  if (flt.k > 0) {
+    const uint32_t t = select_key<false, NT>(items, 1, sc, static_cast<uint64_t>(flt.k), bins, tmp, above);
+    edge = t;
+    ties = static_cast<uint64_t>(flt.k) - above;
+  }
+  if (flt.p < 1.f) {
+    uint64_t over = total;
+    if (flt.k > 0) {  // all above the edge, and `ties` of the items at it (or all, if fewer)
+      uint64_t at_edge = 0;
+      over = 0;
+      items.each([&](int, uint32_t q) {
+        if (q > edge) over += sc.mass(of_key(q));
+        if (q == edge) ++at_edge;
+      });
+      over = block_sum<NT>(over, tmp);
+      at_edge = block_sum<NT>(at_edge, tmp);
+      over += (at_edge < ties ? at_edge : ties) * sc.mass(of_key(edge));
+    }
+    const double want = static_cast<double>(flt.p) * static_cast<double>(over);
+    const uint64_t goal = want > 1.0 ? static_cast<uint64_t>(want) : 1;  // the first item stays
+    const uint32_t t = select_key<true, NT>(items, edge, sc, goal, bins, tmp, above);
+    if (t != 0) {
+      const uint64_t w = sc.mass(of_key(t));
+      const uint64_t n = w > 0 ? (goal - above + w - 1) / w : ~0ull;
+      ties = t > edge ? n : (n < ties ? n : ties);
+      edge = t;
+    }
+  }
+  // the first item, and how many are equal to the edge
+  const uint32_t best = key_of(sc.top);
+  uint32_t first = 0xffffffffu;
+  uint64_t equal = 0;
+  items.each([&](int i, uint32_t q) {
+    if (q == best) first = min(first, static_cast<uint32_t>(i));
+    equal += q == edge;
+  });
+  first = ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp));
+  equal = block_sum<NT>(equal, tmp);
+  uint32_t last = 0xffffffffu;  // the last index kept of the items at the edge
+  if (equal > ties) {
+    // the ties-th of them: their complemented indexes as keys
+    const auto by_index = [&](auto f) { items.each([&](int i, uint32_t q) { f(i, q == edge ? ~static_cast<uint32_t>(i) : 0u); }); };
+    last = ~select_key<false, NT>(Through<decltype(by_index)>{by_index}, 1, sc, ties, bins, tmp, above);
+  }
+  Race race;
+  items.each([&](int i, uint32_t q) {
+    if (q == 0 || q < edge) return;
+    if (q == edge && static_cast<uint32_t>(i) > last) return;
+    if (!(sc.weight(of_key(q)) >= flt.min) && static_cast<uint32_t>(i) != first) return;
+    race.enter(noise ? of_key(q) / divisor - logf(noise[i]) : of_key(q), q, static_cast<uint32_t>(i));
+  });
+  race.block_join<NT>(bins);
+  return race.key ? Drawn{race.key, race.index} : Drawn{best, first};
+}
+
+// The race over a row's kept items: those that rank at or above `last` (key and
+// complemented index) and have min-p's weight.
+template <int NT, typename Items>
+__device__ Drawn race_row(const Items &items, Scale sc, uint64_t last, float least, float divisor, const float *noise,
+                          uint64_t *bins, uint64_t *tmp) {
+  const uint32_t best = key_of(sc.top);
+  uint32_t first = 0xffffffffu;
+  Race race;
+  items.each([&](int i, uint32_t q) {
+    if (q == best) first = min(first, static_cast<uint32_t>(i));
+    if (q == 0 || (static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i)) < last) return;
+    const float y = of_key(q);
+    if (sc.weight(y) >= least) race.enter(y / divisor - logf(noise[i]), q, static_cast<uint32_t>(i));
+  });
+  race.block_join<NT>(bins);
+  if (race.key) return Drawn{race.key, race.index};
+  return Drawn{best, ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp))};
+}
+
+// Top-p alone, for rows whose prefix is long: masses by linear bins of
+// log2 w (1/64 wide, so that few lanes meet in one; a histogram of float
+// bits has its items in a few dozen), then the items of the bin that the
+// edge lies in, sorted.  False if those are too many (equal scores).
+template <int NT, typename Items>
+__device__ bool select_share(const Items &items, Scale sc, Filters flt, float divisor, const float *noise, uint64_t total,
+                             uint64_t *bins, uint64_t *list, int *listed, uint64_t *tmp, Drawn &drawn) {
+  const auto bin_of = [&](uint32_t q) {
+    return min(static_cast<int>((sc.top - of_key(q)) * sc.f * 64.f), kBins - 1);  // the conversion saturates
+  };
+  const double want = static_cast<double>(flt.p) * static_cast<double>(total);
+  const uint64_t goal = want > 1.0 ? static_cast<uint64_t>(want) : 1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += NT) bins[i] = 0;
+  if (threadIdx.x == 0) *listed = 0;
+  __syncthreads();
+  items.each([&](int, uint32_t q) {
+    if (q != 0)
+      atomicAdd(reinterpret_cast<unsigned long long *>(&bins[bin_of(q)]),
+                static_cast<unsigned long long>(sc.mass(of_key(q))));
+  });
+  __syncthreads();
+  constexpr int per = kBins / NT;
+  uint64_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < per; ++j) mine += bins[threadIdx.x * per + j];
+  uint64_t run = mine;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint64_t y = __shfl_up(run, o);
+    if (lane_id() >= o) run += y;
+  }
+  __syncthreads();
+  if (lane_id() == kWave - 1) tmp[threadIdx.x / kWave] = run;
+  __syncthreads();
+  run -= mine;
+  for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
+  int edge = -1;  // the last bin with any mass whose items have less than the goal above them
+  uint64_t edge_above = 0;
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    const uint64_t c = bins[threadIdx.x * per + j];
+    if (c != 0 && run < goal) edge = threadIdx.x * per + j, edge_above = run;
+    run += c;
+  }
+  const int bin = static_cast<int>(block_max<NT>(static_cast<uint64_t>(edge + 1), tmp)) - 1;
+  if (edge == bin) tmp[16] = edge_above;
+  __syncthreads();
+  const uint64_t above = tmp[16];
+  items.each([&](int i, uint32_t q) {
+    if (q != 0 && bin_of(q) == bin) {
+      const int at = atomicAdd(listed, 1);
+      if (at < NT) list[at] = static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i);
+    }
+  });
+  __syncthreads();
+  const int n = *listed;
+  if (n > NT) return false;
+  int size = kWave;
+  while (size < n) size <<= 1;
+  const uint64_t c = block_sort<NT, uint64_t>(static_cast<int>(threadIdx.x) < n ? list[threadIdx.x] : 0ull, size, bins);
+  const bool real = static_cast<int>(threadIdx.x) < n;
+  mine = real ? sc.mass(of_key(static_cast<uint32_t>(c >> 32))) : 0;
+  run = mine;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint64_t y = __shfl_up(run, o);
+    if (lane_id() >= o) run += y;
+  }
+  __syncthreads();
+  if (lane_id() == kWave - 1) tmp[threadIdx.x / kWave] = run;
+  __syncthreads();
+  run += above - mine;
+  for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
+  // the last kept item; complemented, so that the largest is the lowest in rank
+  const uint64_t last = ~block_max<NT>(real && run < goal ? ~c : 0ull, tmp);
+  drawn = race_row<NT>(items, sc, last, flt.min, divisor, noise, bins, tmp);
+  return true;
+}
+
+// kShort: a granule per thread covers the row, and is held; longer rows are
+// read twice (held in registers they spilled, and the second read comes from the caches: 18
+// us instead of 22 for one row of 32,003 fp32 scores, 197 instead of 382 for 256 of 131,072 bf16).
+template <typename T, int NT, bool kShort>
+__global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
+  using G = Granule<T>;
+  __shared__ uint64_t bins[kBins > 2 * NT ? kBins : 2 * NT];
+  __shared__ uint64_t list[NT * G::N < kList ? NT * G::N : kList];
+  __shared__ uint64_t tmp[17];
+  __shared__ int listed;
+  constexpr int kCap = sizeof(list) / 8;
+  const int64_t r = blockIdx.x;
+  const int tid = threadIdx.x, items = static_cast<int>(a.items);
+  const T *x = static_cast<const T *>(a.scores) + r * a.stride;
+  const float *noise = a.noise + r * a.noise_stride;
+  const float t = a.temperature ? a.temperature[r] : 1.f;
+  const bool greedy = !(t > 0.f);
+  const float divisor = greedy ? 1.f : t;
+  Filters flt{a.top_k ? a.top_k[r] : 0, a.top_p ? a.top_p[r] : 1.f, a.min_p ? a.min_p[r] : 0.f};
+  if (flt.k < 0 || flt.k >= items) flt.k = 0;
+  if (!(flt.p < 1.f)) flt.p = 1.f;
+  if (greedy) flt = Filters{items > 1 ? 1 : 0, 1.f, 0.f};
+  const bool open = !greedy && flt.k == 0 && flt.p == 1.f && !(flt.min > 0.f);  // every item may win
+  const float f = fminf(kLog2e / divisor, kMost);
+
+  // 1. maxima, and the sum of w against the thread's own maximum
+  float mine = -__builtin_inff(), ref = -kMost, sum = 0.f;
+  auto take = [&](const G &g) {
+    float y[G::N], top = mine;
+#pragma unroll
+    for (int j = 0; j < G::N; ++j) {
+      y[j] = g.at(j);
+      top = fmaxf(top, y[j]);
+    }
+    mine = top;
+    const float now = fmaxf(ref, top);
+    sum *= __builtin_amdgcn_exp2f((ref - now) * f);
+    ref = now;
+#pragma unroll
+    for (int j = 0; j < G::N; ++j) sum += __builtin_amdgcn_exp2f((y[j] - ref) * f);
+  };
+  constexpr int kAhead = 4;
+  // the granule the row ends in, if it ends within one, is one thread's
+  const int whole_end = items / G::N * G::N;
+  const bool has_end = tid == NT - 1 && whole_end < items;
+  Race race;
+  G held;
+  if (open) {
+    for (int first = tid * G::N; first < items; first += NT * G::N) {
+      G g;
+      float e[G::N];
+      if (first <= items - G::N) {
+        g.load(x, first, items);
+        __builtin_memcpy(e, noise + first, sizeof(e));
+      } else {
+        g.load_end(x, first, items);
+#pragma unroll
+        for (int j = 0; j < G::N; ++j) e[j] = first + j < items ? noise[first + j] : 1.f;
+      }
+      take(g);
+#pragma unroll
+      for (int j = 0; j < G::N; ++j) {
+        const float y = g.at(j);
+        if (y > -__builtin_inff()) race.enter(y / divisor - logf(e[j]), key_of(y), first + j);
+      }
+    }
+  } else if constexpr (kShort) {
+    held.load(x, tid * G::N, items);
+    take(held);
+  } else {
+    for (int first = tid * G::N; first < items; first += kAhead * NT * G::N) {
+      G g[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) g[u].load(x, first + u * NT * G::N, items);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) take(g[u]);
+    }
+  }
+  if (!open && has_end) {
+    G g;
+    g.load_end(x, whole_end, items);
+    take(g);
+  }
+  const uint32_t best = static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(item_key(mine)), tmp));
   if (best == 0) {
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       a.index[r] = -1;
       a.logprob[r] = -__builtin_inff();
     }
     return;
   }
-  const float top = of_key(best);
-  float sum = 0.f;
-  uint32_t first = 0xffffffffu;  // the first item: the lowest index of the best key
-  row.each([&](int i, uint32_t k) {
-    if (k != 0) sum += weight(k, top);
-    if (k == best) first = min(first, static_cast<uint32_t>(i));
-  });
-  sum = block_sum<NT>(sum, tmp);
-  first = ~block_max<NT>(~first, tmp);
+  const Scale sc{of_key(best), f};
+  sum = block_sum<NT>(sum * __builtin_amdgcn_exp2f((ref - sc.top) * f), tmp);
 
-  uint32_t drawn = first, drawn_key = best;
-  if (race) {
-    // the kept prefix: keys above `edge`, and of those equal to it the first `ties` by index
-    uint32_t edge = 1;
-    uint64_t ties = 0xffffffffu;
-    const int k = a.top_k ? a.top_k[r] : 0;
-    if (k > 0 && k < items) {
-      uint64_t above;
-      const uint32_t t = select_key<false, R, NT>(row, 1, top, static_cast<uint64_t>(k), bins, tmp64, above);
-      edge = t;
-      ties = static_cast<uint64_t>(k) - above;
-    }
-    const float p = a.top_p ? a.top_p[r] : 1.f;
-    if (p < 1.f) {
-      // the mass of the first k: all above the edge, and `ties` of the items at it (or all, if fewer)
-      uint64_t over = 0, at_edge = 0;
-      row.each([&](int, uint32_t q) {
-        if (q > edge) over += mass_of(weight(q, top));
-        if (q == edge) ++at_edge;
+  Drawn drawn{best, 0};
+  if (open) {
+    race.block_join<NT>(bins);
+    drawn = Drawn{race.key, race.index};
+    if (race.key == 0) {  // no score is a number (the noise is not): the first item
+      uint32_t first = 0xffffffffu;
+      RowItems<T, NT>{x, items}.each([&](int i, uint32_t q) {
+        if (q == best) first = min(first, static_cast<uint32_t>(i));
       });
-      over = block_sum64<NT>(over, tmp64);
-      at_edge = block_sum64<NT>(at_edge, tmp64);
-      if (at_edge > 0) over += min(at_edge, ties) * mass_of(weight(edge, top));
-      const double target = static_cast<double>(p) * static_cast<double>(over);
-      uint64_t goal = target > 1.0 ? static_cast<uint64_t>(target) : 1;  // the first item stays
-      uint64_t above;
-      const uint32_t t = select_key<true, R, NT>(row, edge, top, goal, bins, tmp64, above);
-      if (t != 0) {
-        const uint64_t w = mass_of(weight(t, top));
-        const uint64_t n = w > 0 ? (goal - above + w - 1) / w : 0xffffffffull;
-        if (t > edge)
-          ties = n;
-        else
-          ties = n < ties ? n : ties;
-        edge = t;
-      }
+      drawn = Drawn{best, ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp))};
     }
-    // items equal to the edge: how many there are, and where the kept ones end
-    uint32_t equal = 0;
-    row.each([&](int, uint32_t q) { equal += q == edge; });
-    equal = static_cast<uint32_t>(block_sum64<NT>(equal, tmp64));
-    uint32_t last = 0xffffffffu;
-    if (equal > ties) {
-      if (threadIdx.x == 0) cut = 0xffffffffu;
+  } else {
+    // 2. the bound, and the list of the items that reach it
+    uint32_t rank_bound = 1, min_bound = 1;
+    if (items > NT) {
+      const int owners = min(NT, items / G::N);
+      const int rank = flt.k > 0 ? flt.k : owners / 2;
+      if (rank <= owners && (flt.k > 0 || flt.p < 1.f)) {
+        const uint32_t m = block_sort<NT, uint32_t>(item_key(mine), NT, reinterpret_cast<uint32_t *>(bins));
+        __syncthreads();
+        if (tid == rank - 1) tmp[16] = m;
+        __syncthreads();
+        rank_bound = max(static_cast<uint32_t>(tmp[16]), 1u);
+      }
+      // a little below min-p's own bound (its test follows per item); top-p's share of the first k needs all of those
+      if (flt.min > 0.f && !(flt.k > 0 && flt.p < 1.f))
+        min_bound = max(min(item_key(clean(sc.top + (log2f(flt.min) - 0.01f) / f)), best), 1u);
+    }
+    // with the rank's bound first; where that list doesn't hold the prefix, with min-p's own
+    bool whole = false;
+    for (int attempt = 0; attempt < 2 && !whole; ++attempt) {
+      const uint32_t bound = attempt == 0 ? max(rank_bound, min_bound) : min_bound;
+      if (attempt == 1 && (min_bound == 1 || min_bound >= rank_bound)) break;
       __syncthreads();
-      uint32_t seen = 0;
-      for (int base = 0; base < items && seen < ties; base += NT) {
-        const int i = base + threadIdx.x;
-        const bool is = i < items && row.make(i) == edge;
-        const uint64_t m = ballot(is);
-        if (lane_id() == 0) tmp[threadIdx.x / kWave] = __popcll(m);
-        __syncthreads();
-        uint32_t before = seen, all = 0;
-        for (int w = 0; w < NT / kWave; ++w) {
-          if (w < static_cast<int>(threadIdx.x) / kWave) before += tmp[w];
-          all += tmp[w];
-        }
-        before += __popcll(m & lanemask_lt());
-        if (is && before + 1 == ties) cut = static_cast<uint32_t>(i);
-        seen += all;
-        __syncthreads();
-      }
-      last = cut;
-    }
-    const float least = a.min_p ? a.min_p[r] : 0.f;
-    const float *noise = a.noise + r * a.noise_stride;
-    // the race: by z - log(noise), then by rank
-    float s_best = -__builtin_inff();
-    uint32_t i_best = first, k_best = best;
-    bool any = false;
-    row.each([&](int i, uint32_t q) {
-      if (q < edge || q == 0) return;
-      if (q == edge && static_cast<uint32_t>(i) > last) return;
-      if (q != best && !(weight(q, top) >= least)) return;
-      if (q == best && static_cast<uint32_t>(i) != first && !(1.f >= least)) return;
-      const float s = of_key(q) - logf(noise[i]);
-      const bool better = !any || s > s_best || (s == s_best && (q > k_best || (q == k_best && static_cast<uint32_t>(i) < i_best)));
-      if (better && s == s) {
-        s_best = s;
-        i_best = static_cast<uint32_t>(i);
-        k_best = q;
-        any = true;
-      }
-    });
-    uint64_t packed = any ? (static_cast<uint64_t>(key_of(s_best)) << 32 | ~i_best) : 0ull;
-    // over the wave and the block, in order of (score, key, index)
+      if (tid == 0) listed = 0;
+      __syncthreads();
+      const float floor = of_key(bound);
+      auto put = [&](const G &g, int first) {
+        float y[G::N], top = -__builtin_inff();
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      const uint64_t y = __shfl_xor(packed, o);
-      const uint32_t yk = static_cast<uint32_t>(__shfl_xor(static_cast<int>(k_best), o));
-      const uint32_t ps = packed >> 32, ys = y >> 32;
-      if (ys > ps || (ys == ps && (yk > k_best || (yk == k_best && y > packed)))) packed = y, k_best = yk;
+        for (int j = 0; j < G::N; ++j) {
+          y[j] = g.at(j);
+          top = fmaxf(top, y[j]);
+        }
+        if (bound == 1 ? top > -__builtin_inff() : top >= floor) {
+#pragma unroll
+          for (int j = 0; j < G::N; ++j) {
+            const uint32_t k = item_key(y[j]);
+            if (k >= bound) {
+              const int at = atomicAdd(&listed, 1);
+              if (at < kCap) list[at] = static_cast<uint64_t>(k) << 32 | ~static_cast<uint32_t>(first + j);
+            }
+          }
+        }
+      };
+      if constexpr (kShort) {
+        put(held, tid * G::N);
+      } else {
+        for (int first = tid * G::N; first < items; first += kAhead * NT * G::N) {
+          G g[kAhead];
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) g[u].load(x, first + u * NT * G::N, items);
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) put(g[u], first + u * NT * G::N);
+        }
+      }
+      if (has_end) {
+        G g;
+        g.load_end(x, whole_end, items);
+        put(g, whole_end);
+      }
+      __syncthreads();
+      const int n = listed;
+      whole = n <= kCap;  // the list holds every item that reaches the bound
+      if (whole && n <= NT) {
+        // 3. the sorted list
+        int size = kWave;
+        while (size < n) size <<= 1;
+        const uint64_t c = block_sort<NT, uint64_t>(tid < n ? list[tid] : 0ull, size, bins);
+        const uint32_t key = static_cast<uint32_t>(c >> 32), at = ~static_cast<uint32_t>(c);
+        const bool real = tid < n;
+        const float y = real ? of_key(key) : 0.f, w = real ? sc.weight(y) : 0.f;
+        float incl = w;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+          const float z = __shfl_up(incl, o);
+          if (lane_id() >= o) incl += z;
+        }
+        float *waves = reinterpret_cast<float *>(tmp);
+        __syncthreads();
+        if (lane_id() == kWave - 1) waves[tid / kWave] = incl;
+        __syncthreads();
+        float before = incl - w, all = 0.f;
+        for (int v = 0; v < NT / kWave; ++v) {
+          if (v < tid / kWave) before += waves[v];
+          all += waves[v];
+        }
+        float mass = sum;  // what top-p is a share of
+        if (flt.k > 0 && flt.p < 1.f) {
+          if (tid == min(flt.k, n) - 1) tmp[16] = __builtin_bit_cast(uint32_t, before + w);
+          __syncthreads();
+          mass = __builtin_bit_cast(float, static_cast<uint32_t>(tmp[16]));
+        }
+        // without top-k the list has to reach top-p's share, or min-p's bound
+        whole = flt.k > 0 || bound == 1 || all >= flt.p * mass ||
+                (min_bound > 1 && bound == min_bound);
+        if (whole) {
+          const bool keep = real && (tid == 0 || ((flt.k == 0 || tid < flt.k) &&
+                                                  (flt.p == 1.f || before < flt.p * mass) && w >= flt.min));
+          uint64_t run = 0;
+          if (keep) {
+            const float s = greedy ? y : y / divisor - logf(noise[at]);
+            if (s == s) run = static_cast<uint64_t>(key_of(s)) << 32 | ~static_cast<uint32_t>(tid);
+          }
+          run = block_max<NT>(run, tmp);
+          const int winner = run ? static_cast<int>(~static_cast<uint32_t>(run)) : 0;
+          __syncthreads();
+          if (tid == winner) tmp[16] = c;
+          __syncthreads();
+          drawn = Drawn{static_cast<uint32_t>(tmp[16] >> 32), ~static_cast<uint32_t>(tmp[16])};
+        }
+      } else if (whole) {
+        // a longer list: it has to hold the prefix, as above
+        ListItems<NT> li{list, n};
+        uint64_t all = 0;
+        li.each([&](int, uint32_t q) { all += sc.mass(of_key(q)); });
+        all = block_sum<NT>(all, tmp);
+        const uint64_t total = static_cast<uint64_t>(sum * kMass);
+        whole = flt.k > 0 || bound == 1 || static_cast<double>(all) >= static_cast<double>(flt.p) * static_cast<double>(total) ||
+                (min_bound > 1 && bound == min_bound);
+        if (whole) drawn = select_prefix<NT>(li, sc, flt, divisor, greedy ? nullptr : noise, total, bins, tmp);
+      }
     }
-    if (lane_id() == 0) race_key[threadIdx.x / kWave] = packed, race_z[threadIdx.x / kWave] = k_best;
-    __syncthreads();
-    packed = race_key[0];
-    k_best = race_z[0];
-    for (int w = 1; w < NT / kWave; ++w) {
-      const uint64_t y = race_key[w];
-      const uint32_t yk = race_z[w];
-      const uint32_t ps = packed >> 32, ys = y >> 32;
-      if (ys > ps || (ys == ps && (yk > k_best || (yk == k_best && y > packed)))) packed = y, k_best = yk;
-    }
-    if (packed != 0) {
-      drawn = ~static_cast<uint32_t>(packed);
-      drawn_key = k_best;
+    if (!whole) {
+      RowItems<T, NT> row{x, items};
+      const uint64_t total = static_cast<uint64_t>(sum * kMass);
+      if (flt.k == 0 && flt.p == 1.f)
+        drawn = race_row<NT>(row, sc, 0, flt.min, divisor, noise, bins, tmp);
+      else if (flt.k > 0 || !select_share<NT>(row, sc, flt, divisor, noise, total, bins, list, &listed, tmp, drawn))
+        drawn = select_prefix<NT>(row, sc, flt, divisor, greedy ? nullptr : noise, total, bins, tmp);
     }
   }
-  if (threadIdx.x == 0) {
-    a.index[r] = drawn;
-    a.logprob[r] = (of_key(drawn_key) - top) - logf(sum);
+  if (tid == 0) {
+    a.index[r] = drawn.index;
+    a.logprob[r] = (of_key(drawn.key) - sc.top) / divisor - logf(sum);
   }
 }
 
+// Threads by the row's length: one item per thread of a sort where the row is
+// that short.
 template <typename T>
 void launch(const SampleArgs &a, int64_t rows, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(rows);
-  if (a.items <= 256 * 8)
-    sample_kernel<T, 256, 8><<<grid, 256, 0, stream>>>(a);
-  else if (a.items <= 1024 * 32)
-    sample_kernel<T, 1024, 32><<<grid, 1024, 0, stream>>>(a);
+  constexpr int N = Granule<T>::N;
+  if (a.items <= 256)
+    sample_kernel<T, 256, true><<<grid, 256, 0, stream>>>(a);
+  else if (a.items <= 1024 * N)
+    sample_kernel<T, 1024, true><<<grid, 1024, 0, stream>>>(a);
   else
-    sample_kernel<T, 1024, 0><<<grid, 1024, 0, stream>>>(a);
+    sample_kernel<T, 1024, false><<<grid, 1024, 0, stream>>>(a);
 }
 
 }  // namespace
