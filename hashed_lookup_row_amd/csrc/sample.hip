@@ -25,8 +25,9 @@
 // large top-p, many equal scores), the prefix is found as a threshold over the
 // list or the row itself: for top-p alone by linear bins of log2 w
 // (select_share), else by a radix selection (select_prefix), by counts
-// for top-k, by masses in whole numbers of 2^-36 for top-p, so that no result hangs
-// on the order of atomics.
+// for top-k, by masses for top-p.  Masses are whole numbers in units of the
+// total's 2^-31, so that no result hangs on the order of atomics; top-p's share
+// is taken of their own sum.
 #include "hlr_common.hpp"
 #include "hist_common.hpp"
 
@@ -37,7 +38,7 @@ using namespace hlr;
 
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
-constexpr float kMass = 68719476736.f;  // 2^36
+constexpr float kUnits = 2147483648.f;  // 2^31
 constexpr int kBins = 2048;
 constexpr int kList = 4096;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -71,10 +72,9 @@ struct SampleArgs {
 // What a row's items are measured against.
 struct Scale {
   float top, f;  // the largest x; log2(e) / temperature
+  float units;   // of mass per weight: 2^31 over a bound of the weights that are added up
   __device__ __forceinline__ float weight(float x) const { return __builtin_amdgcn_exp2f((x - top) * f); }
-  __device__ __forceinline__ uint64_t mass(float x) const {
-    return static_cast<uint64_t>(__builtin_rintf(weight(x) * kMass));
-  }
+  __device__ __forceinline__ uint32_t mass(float x) const { return static_cast<uint32_t>(weight(x) * units + 0.5f); }
 };
 
 // A granule: 16 bytes of scores, of any alignment.
@@ -121,23 +121,41 @@ struct Granule {
   }
 };
 
-// The whole row, from memory.
+// The whole row, from memory, four granules in flight per thread.
 template <typename T, int NT>
 struct RowItems {
+  using G = Granule<T>;
   const T *x;
   int items;
   template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-    using G = Granule<T>;
-    for (int first = threadIdx.x * G::N; first < items; first += NT * G::N) {
-      G g;
-      if (first <= items - G::N)
-        g.load(x, first, items);
-      else
-        g.load_end(x, first, items);
+  __device__ __forceinline__ void each_granule(F f) const {
+    constexpr int kAhead = 4;
+    int first = threadIdx.x * G::N;
+    for (; first < items; first += kAhead * NT * G::N) {
+      G g[kAhead];
 #pragma unroll
-      for (int j = 0; j < G::N; ++j) f(first + j, item_key(g.at(j)));
+      for (int u = 0; u < kAhead; ++u) g[u].load(x, first + u * NT * G::N, items);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) f(first + u * NT * G::N, g[u]);
     }
+    const int end = items / G::N * G::N;  // the granule the row ends in, if it ends within one, is one thread's
+    if (threadIdx.x == NT - 1 && end < items) {
+      G g;
+      g.load_end(x, end, items);
+      f(end, g);
+    }
+  }
+  // Scores: -inf for items that can't be drawn.
+  template <typename F>
+  __device__ __forceinline__ void each_score(F f) const {
+    each_granule([&](int first, const G &g) {
+#pragma unroll
+      for (int j = 0; j < G::N; ++j) f(first + j, g.at(j));
+    });
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    each_score([&](int i, float y) { f(i, item_key(y)); });
   }
 };
 
@@ -238,11 +256,28 @@ __device__ __forceinline__ uint64_t from_lane_xor(uint64_t v) {
          from_lane_xor<J>(static_cast<uint32_t>(v));
 }
 
+// The lanes whose bit J is clear (J below 64).
+constexpr uint64_t lanes_without(int J) {
+  uint64_t m = 0;
+  for (int i = 0; i < kWave; ++i)
+    if ((i & J) == 0) m |= 1ull << i;
+  return m;
+}
 // One step of the bitonic network: the larger of v and y goes to the thread
-// whose bits J and K are alike.
+// whose bits J and K are alike.  In a wave those are lanes known at compile
+// time, all or none of them flipped where K is a bit of the wave's number.
 template <int K, int J, typename U>
 __device__ __forceinline__ U keep(U v, U y) {
-  const bool larger = ((threadIdx.x & J) == 0) == ((threadIdx.x & K) == 0);
+  bool larger;
+  if constexpr (J < kWave && K < kWave)
+    larger = __builtin_amdgcn_inverse_ballot_w64(~(lanes_without(J) ^ lanes_without(K)));
+  else {
+    const bool k = (__builtin_amdgcn_readfirstlane(threadIdx.x) & K) == 0;
+    if constexpr (J < kWave)
+      larger = __builtin_amdgcn_inverse_ballot_w64(k ? lanes_without(J) : ~lanes_without(J));
+    else
+      larger = ((__builtin_amdgcn_readfirstlane(threadIdx.x) & J) == 0) == k;
+  }
   return (v > y) == larger ? v : y;
 }
 template <int K, int J, typename U>
@@ -252,39 +287,40 @@ __device__ __forceinline__ U merge_in_wave(U v) {
   return v;
 }
 template <int NT, int K, int J, typename U>
-__device__ __forceinline__ U merge(U v, U *buf, int &turn) {
+__device__ __forceinline__ U merge(U v, bool counts, U *buf, int &turn) {
   if constexpr (J >= kWave) {
     U *b = buf + (turn ^= 1) * NT;  // the buffers take turns, so one barrier per step is enough
-    b[threadIdx.x] = v;
+    if (counts) b[threadIdx.x] = v;
     __syncthreads();
-    v = keep<K, J>(v, b[threadIdx.x ^ J]);
-    return merge<NT, K, J / 2>(v, buf, turn);
+    if (counts) v = keep<K, J>(v, b[threadIdx.x ^ J]);
+    return merge<NT, K, J / 2>(v, counts, buf, turn);
   } else {
-    return merge_in_wave<K, J>(v);
+    return counts ? merge_in_wave<K, J>(v) : v;
   }
 }
 template <int NT, int K, typename U>
-__device__ __forceinline__ U sort_from(U v, int size, U *buf, int &turn) {
+__device__ __forceinline__ U sort_from(U v, int size, bool counts, U *buf, int &turn) {
   if (K > size) return v;
-  v = merge<NT, K, K / 2>(v, buf, turn);
-  if constexpr (K < NT) v = sort_from<NT, 2 * K>(v, size, buf, turn);
+  v = merge<NT, K, K / 2>(v, counts, buf, turn);
+  if constexpr (K < NT) v = sort_from<NT, 2 * K>(v, size, counts, buf, turn);
   return v;
 }
-// Sorts one value per thread in descending order by the bitonic network, in
-// runs of `size` (a power of two from 64); buf holds 2 NT.
+// Sorts one value per thread of the first `size` threads (a power of two from
+// 64) in descending order by the bitonic network; buf holds 2 NT.
 template <int NT, typename U>
 __device__ __forceinline__ U block_sort(U v, int size, U *buf) {
   int turn = 0;
   __syncthreads();
-  return sort_from<NT, 2>(v, size, buf, turn);
+  return sort_from<NT, 2>(v, size, static_cast<int>(threadIdx.x) < size, buf, turn);
 }
 
 // Finds, among the items with key >= floor, the lowest key t above which the
 // total is still below `target`; `above` receives the total above t.  Totals are
 // counts (kMassed false) or masses.
 template <bool kMassed, int NT, typename Items>
-__device__ uint32_t select_key(const Items &items, uint32_t floor, Scale sc, uint64_t target, uint64_t *bins,
+__device__ uint32_t select_key(const Items &items, uint32_t floor, Scale sc, uint64_t target, uint64_t *buf,
                                uint64_t *tmp, uint64_t &above) {
+  uint32_t *bins = reinterpret_cast<uint32_t *>(buf);
   uint32_t prefix = 0, mask = 0;
   above = 0;
   const int shifts[3] = {21, 10, 0}, widths[3] = {11, 11, 10};
@@ -296,8 +332,7 @@ __device__ uint32_t select_key(const Items &items, uint32_t floor, Scale sc, uin
     __syncthreads();
     items.each([&](int, uint32_t k) {
       if (k != 0 && k >= floor && (k & mask) == prefix)
-        atomicAdd(reinterpret_cast<unsigned long long *>(&bins[(k >> shift) & field]),
-                  static_cast<unsigned long long>(kMassed ? sc.mass(of_key(k)) : 1));
+        atomicAdd(&bins[(k >> shift) & field], kMassed ? sc.mass(of_key(k)) : 1u);
     });
     __syncthreads();
     // bins descend in rank; the last non-empty one whose total above is below the target
@@ -321,7 +356,7 @@ __device__ uint32_t select_key(const Items &items, uint32_t floor, Scale sc, uin
     uint64_t best_above = 0;
 #pragma unroll
     for (int j = 0; j < per; ++j) {
-      const uint64_t c = bins[b0 - j];
+      const uint32_t c = bins[b0 - j];
       if (c != 0 && run < target) best = kBins - 1 - (b0 - j), best_above = run;
       run += c;
     }
@@ -382,11 +417,17 @@ struct Race {
   }
 };
 
-// The kept prefix as a threshold, over items in any order; total: the mass
-// of all items where top-k is off.
+// top-p's share of a mass; at least 1, so that the first item stays.
+__device__ __forceinline__ uint64_t share_of(uint64_t total, float p) {
+  const double want = static_cast<double>(p) * static_cast<double>(total);
+  return want > 1.0 ? static_cast<uint64_t>(want) : 1;
+}
+
+// The kept prefix as a threshold, over items in any order.  all: the items are
+// the whole row (else, without top-k, the row's mass is 2^31 units).
 template <int NT, typename Items>
 __device__ Drawn select_prefix(const Items &items, Scale sc, Filters flt, float divisor, const float *noise,
-                               uint64_t total, uint64_t *bins, uint64_t *tmp) {
+                               bool all, uint64_t *bins, uint64_t *tmp) {
   uint32_t edge = 1;  // kept: keys above `edge`, and of those equal to it the first `ties` by index
   uint64_t ties = ~0ull, above;
   if (flt.k > 0) {
@@ -395,26 +436,28 @@ __device__ Drawn select_prefix(const Items &items, Scale sc, Filters flt, float 
     ties = static_cast<uint64_t>(flt.k) - above;
   }
   if (flt.p < 1.f) {
-    uint64_t over = total;
-    if (flt.k > 0) {  // all above the edge, and `ties` of the items at it (or all, if fewer)
-      uint64_t at_edge = 0;
-      over = 0;
-      items.each([&](int, uint32_t q) {
-        if (q > edge) over += sc.mass(of_key(q));
-        if (q == edge) ++at_edge;
-      });
-      over = block_sum<NT>(over, tmp);
-      at_edge = block_sum<NT>(at_edge, tmp);
-      over += (at_edge < ties ? at_edge : ties) * sc.mass(of_key(edge));
-    }
-    const double want = static_cast<double>(flt.p) * static_cast<double>(over);
-    const uint64_t goal = want > 1.0 ? static_cast<uint64_t>(want) : 1;  // the first item stays
-    const uint32_t t = select_key<true, NT>(items, edge, sc, goal, bins, tmp, above);
-    if (t != 0) {
-      const uint64_t w = sc.mass(of_key(t));
-      const uint64_t n = w > 0 ? (goal - above + w - 1) / w : ~0ull;
-      ties = t > edge ? n : (n < ties ? n : ties);
-      edge = t;
+    // the mass above the edge, and with `ties` of the items at it (or all, if fewer)
+    uint64_t above_edge = 0, at_edge = 0;
+    items.each([&](int, uint32_t q) {
+      if (q > edge) above_edge += sc.mass(of_key(q));
+      if (q == edge) ++at_edge;
+    });
+    above_edge = block_sum<NT>(above_edge, tmp);
+    at_edge = block_sum<NT>(at_edge, tmp);
+    const uint64_t w = flt.k > 0 ? sc.mass(of_key(edge)) : 0;
+    uint64_t total = above_edge + (at_edge < ties ? at_edge : ties) * w;
+    if (flt.k == 0 && !all) total = static_cast<uint64_t>(kUnits);
+    const uint64_t goal = share_of(total, flt.p);
+    if (flt.k > 0 && above_edge < goal) {
+      const uint64_t n = w > 0 ? (goal - above_edge + w - 1) / w : ~0ull;
+      ties = n < ties ? n : ties;
+    } else {
+      const uint32_t t = select_key<true, NT>(items, edge + 1, sc, goal, bins, tmp, above);
+      if (t != 0) {
+        const uint64_t wt = sc.mass(of_key(t));
+        ties = wt > 0 ? (goal - above + wt - 1) / wt : ~0ull;
+        edge = t;
+      }
     }
   }
   // the first item, and how many are equal to the edge
@@ -446,17 +489,35 @@ __device__ Drawn select_prefix(const Items &items, Scale sc, Filters flt, float 
 
 // The race over a row's kept items: those that rank at or above `last` (key and
 // complemented index) and have min-p's weight.
-template <int NT, typename Items>
-__device__ Drawn race_row(const Items &items, Scale sc, uint64_t last, float least, float divisor, const float *noise,
+template <typename T, int NT>
+__device__ Drawn race_row(const RowItems<T, NT> &row, Scale sc, uint64_t last, float least, float divisor, const float *noise,
                           uint64_t *bins, uint64_t *tmp) {
-  const uint32_t best = key_of(sc.top);
+  using G = Granule<T>;
+  const uint32_t best = key_of(sc.top), last_key = static_cast<uint32_t>(last >> 32);
+  const float lowest = of_key(max(last_key, 1u));  // of the kept scores; NaN (nothing is below it) if all are
   uint32_t first = 0xffffffffu;
   Race race;
-  items.each([&](int i, uint32_t q) {
-    if (q == best) first = min(first, static_cast<uint32_t>(i));
-    if (q == 0 || (static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i)) < last) return;
-    const float y = of_key(q);
-    if (sc.weight(y) >= least) race.enter(y / divisor - logf(noise[i]), q, static_cast<uint32_t>(i));
+  row.each_granule([&](int at, const G &g) {
+    float y[G::N], top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < G::N; ++j) {
+      y[j] = g.at(j);
+      top = fmaxf(top, y[j]);
+    }
+    if (!(top > -__builtin_inff()) || top < lowest || !(sc.weight(top) >= least || top == sc.top)) return;
+    uint32_t kept = 0;
+#pragma unroll
+    for (int j = 0; j < G::N; ++j) {
+      const uint32_t q = item_key(y[j]), i = at + j;
+      if (q == best) first = min(first, i);
+      if (q != 0 && (static_cast<uint64_t>(q) << 32 | ~i) >= last && sc.weight(y[j]) >= least) kept |= 1u << j;
+    }
+    while (kept) {  // few of a granule's items are kept: as many turns as the lane with the most has
+      const int j = __builtin_ctz(kept), i = at + j;
+      kept &= kept - 1;
+      const float x = clean(static_cast<float>(row.x[i]));
+      race.enter(x / divisor - logf(noise[i]), item_key(x), i);
+    }
   });
   race.block_join<NT>(bins);
   if (race.key) return Drawn{race.key, race.index};
@@ -467,23 +528,27 @@ __device__ Drawn race_row(const Items &items, Scale sc, uint64_t last, float lea
 // log2 w (1/64 wide, so that few lanes meet in one; a histogram of float
 // bits has its items in a few dozen), then the items of the bin that the
 // edge lies in, sorted.  False if those are too many (equal scores).
-template <int NT, typename Items>
-__device__ bool select_share(const Items &items, Scale sc, Filters flt, float divisor, const float *noise, uint64_t total,
-                             uint64_t *bins, uint64_t *list, int *listed, uint64_t *tmp, Drawn &drawn) {
-  const auto bin_of = [&](uint32_t q) {
-    return min(static_cast<int>((sc.top - of_key(q)) * sc.f * 64.f), kBins - 1);  // the conversion saturates
+template <typename T, int NT>
+__device__ bool select_share(const RowItems<T, NT> &items, Scale sc, Filters flt, float divisor, const float *noise,
+                             uint64_t *buf, uint64_t *list, int *listed, uint64_t *tmp, Drawn &drawn) {
+  uint32_t *bins = reinterpret_cast<uint32_t *>(buf);
+  const auto bin_of = [&](float y) {
+    return min(static_cast<int>((sc.top - y) * sc.f * 64.f), kBins - 1);  // the conversion saturates
   };
-  const double want = static_cast<double>(flt.p) * static_cast<double>(total);
-  const uint64_t goal = want > 1.0 ? static_cast<uint64_t>(want) : 1;
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += NT) bins[i] = 0;
   if (threadIdx.x == 0) *listed = 0;
   __syncthreads();
-  items.each([&](int, uint32_t q) {
-    if (q != 0)
-      atomicAdd(reinterpret_cast<unsigned long long *>(&bins[bin_of(q)]),
-                static_cast<unsigned long long>(sc.mass(of_key(q))));
+  // All items below `far` together hold less than top-p leaves out: they can't
+  // be at the edge, and are most of a long row.
+  const float far = fminf(log2f(static_cast<float>(items.items) * sc.units / (kUnits * (1.f - flt.p))) + 0.01f, 1e9f);
+  uint64_t total = 0;
+  items.each_score([&](int, float y) {
+    const uint32_t m = sc.mass(y);  // 0 for -inf
+    total += m;
+    if ((sc.top - y) * sc.f < far) atomicAdd(&bins[bin_of(y)], m);
   });
+  const uint64_t goal = share_of(block_sum<NT>(total, tmp), flt.p);
   __syncthreads();
   constexpr int per = kBins / NT;
   uint64_t mine = 0;
@@ -504,7 +569,7 @@ __device__ bool select_share(const Items &items, Scale sc, Filters flt, float di
   uint64_t edge_above = 0;
 #pragma unroll
   for (int j = 0; j < per; ++j) {
-    const uint64_t c = bins[threadIdx.x * per + j];
+    const uint32_t c = bins[threadIdx.x * per + j];
     if (c != 0 && run < goal) edge = threadIdx.x * per + j, edge_above = run;
     run += c;
   }
@@ -512,10 +577,10 @@ __device__ bool select_share(const Items &items, Scale sc, Filters flt, float di
   if (edge == bin) tmp[16] = edge_above;
   __syncthreads();
   const uint64_t above = tmp[16];
-  items.each([&](int i, uint32_t q) {
-    if (q != 0 && bin_of(q) == bin) {
+  items.each_score([&](int i, float y) {
+    if (bin_of(y) == bin && y > -__builtin_inff()) {
       const int at = atomicAdd(listed, 1);
-      if (at < NT) list[at] = static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i);
+      if (at < NT) list[at] = static_cast<uint64_t>(key_of(y)) << 32 | ~static_cast<uint32_t>(i);
     }
   });
   __syncthreads();
@@ -523,7 +588,7 @@ __device__ bool select_share(const Items &items, Scale sc, Filters flt, float di
   if (n > NT) return false;
   int size = kWave;
   while (size < n) size <<= 1;
-  const uint64_t c = block_sort<NT, uint64_t>(static_cast<int>(threadIdx.x) < n ? list[threadIdx.x] : 0ull, size, bins);
+  const uint64_t c = block_sort<NT, uint64_t>(static_cast<int>(threadIdx.x) < n ? list[threadIdx.x] : 0ull, size, buf);
   const bool real = static_cast<int>(threadIdx.x) < n;
   mine = real ? sc.mass(of_key(static_cast<uint32_t>(c >> 32))) : 0;
   run = mine;
@@ -539,7 +604,7 @@ __device__ bool select_share(const Items &items, Scale sc, Filters flt, float di
   for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
   // the last kept item; complemented, so that the largest is the lowest in rank
   const uint64_t last = ~block_max<NT>(real && run < goal ? ~c : 0ull, tmp);
-  drawn = race_row<NT>(items, sc, last, flt.min, divisor, noise, bins, tmp);
+  drawn = race_row(items, sc, last, flt.min, divisor, noise, buf, tmp);
   return true;
 }
 
@@ -549,7 +614,7 @@ __device__ bool select_share(const Items &items, Scale sc, Filters flt, float di
 template <typename T, int NT, bool kShort>
 __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   using G = Granule<T>;
-  __shared__ uint64_t bins[kBins > 2 * NT ? kBins : 2 * NT];
+  __shared__ uint64_t bins[kBins / 2 > 2 * NT ? kBins / 2 : 2 * NT];  // a histogram, or a sort's buffers
   __shared__ uint64_t list[NT * G::N < kList ? NT * G::N : kList];
   __shared__ uint64_t tmp[17];
   __shared__ int listed;
@@ -584,10 +649,10 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
 #pragma unroll
     for (int j = 0; j < G::N; ++j) sum += __builtin_amdgcn_exp2f((y[j] - ref) * f);
   };
-  constexpr int kAhead = 4;
   // the granule the row ends in, if it ends within one, is one thread's
   const int whole_end = items / G::N * G::N;
   const bool has_end = tid == NT - 1 && whole_end < items;
+  const RowItems<T, NT> row{x, items};
   Race race;
   G held;
   if (open) {
@@ -613,15 +678,9 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
     held.load(x, tid * G::N, items);
     take(held);
   } else {
-    for (int first = tid * G::N; first < items; first += kAhead * NT * G::N) {
-      G g[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) g[u].load(x, first + u * NT * G::N, items);
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) take(g[u]);
-    }
+    row.each_granule([&](int, const G &g) { take(g); });
   }
-  if (!open && has_end) {
+  if (kShort && !open && has_end) {
     G g;
     g.load_end(x, whole_end, items);
     take(g);
@@ -634,8 +693,8 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
     }
     return;
   }
-  const Scale sc{of_key(best), f};
-  sum = block_sum<NT>(sum * __builtin_amdgcn_exp2f((ref - sc.top) * f), tmp);
+  sum = block_sum<NT>(sum * __builtin_amdgcn_exp2f((ref - of_key(best)) * f), tmp);
+  const Scale sc{of_key(best), f, kUnits / (flt.k > 0 ? fminf(sum, static_cast<float>(flt.k)) : sum)};
 
   Drawn drawn{best, 0};
   if (open) {
@@ -643,7 +702,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
     drawn = Drawn{race.key, race.index};
     if (race.key == 0) {  // no score is a number (the noise is not): the first item
       uint32_t first = 0xffffffffu;
-      RowItems<T, NT>{x, items}.each([&](int i, uint32_t q) {
+      row.each([&](int i, uint32_t q) {
         if (q == best) first = min(first, static_cast<uint32_t>(i));
       });
       drawn = Drawn{best, ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp))};
@@ -651,29 +710,53 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   } else {
     // 2. the bound, and the list of the items that reach it
     uint32_t rank_bound = 1, min_bound = 1;
+    bool by_rank = true, by_min = false;  // which bounds are worth a list
     if (items > NT) {
       const int owners = min(NT, items / G::N);
       const int rank = flt.k > 0 ? flt.k : owners / 2;
       if (rank <= owners && (flt.k > 0 || flt.p < 1.f)) {
-        const uint32_t m = block_sort<NT, uint32_t>(item_key(mine), NT, reinterpret_cast<uint32_t *>(bins));
+        uint32_t *buf = reinterpret_cast<uint32_t *>(bins);
+        uint32_t m = item_key(mine);
+        int size = NT;
+        if (flt.k > 0 && flt.k <= NT / 8 && owners == NT) {  // maxima of four threads will do: fewer to sort
+          m = max(m, from_lane_xor<1>(m));
+          m = max(m, from_lane_xor<2>(m));
+          __syncthreads();
+          if (tid % 4 == 0) buf[tid / 4] = m;
+          __syncthreads();
+          size = NT / 4 < kWave ? kWave : NT / 4;
+          m = tid < NT / 4 ? buf[tid] : 0u;
+        }
+        m = block_sort<NT, uint32_t>(m, size, buf);
         __syncthreads();
         if (tid == rank - 1) tmp[16] = m;
         __syncthreads();
         rank_bound = max(static_cast<uint32_t>(tmp[16]), 1u);
+        // without top-k the list has to reach top-p's share: its items weigh about 1.4 times their threads' maxima
+        if (flt.k == 0) {
+          const float some = block_sum<NT>(tid < rank && m != 0 ? sc.weight(of_key(m)) : 0.f, tmp);
+          by_rank = 2.f * some >= flt.p * sum;
+        }
       }
       // a little below min-p's own bound (its test follows per item); top-p's share of the first k needs all of those
-      if (flt.min > 0.f && !(flt.k > 0 && flt.p < 1.f))
+      if (flt.min > 0.f && !(flt.k > 0 && flt.p < 1.f)) {
         min_bound = max(min(item_key(clean(sc.top + (log2f(flt.min) - 0.01f) / f)), best), 1u);
+        // the list overflows (4,096 items) where nearly every thread's maximum reaches the bound
+        const uint64_t reach = block_sum<NT>(static_cast<uint64_t>(item_key(mine) >= min_bound), tmp);
+        by_min = static_cast<int>(reach) * 64 <= owners * 63;
+      }
+      if (flt.k == 0 && flt.p == 1.f) by_rank = false;
     }
     // with the rank's bound first; where that list doesn't hold the prefix, with min-p's own
     bool whole = false;
     for (int attempt = 0; attempt < 2 && !whole; ++attempt) {
       const uint32_t bound = attempt == 0 ? max(rank_bound, min_bound) : min_bound;
-      if (attempt == 1 && (min_bound == 1 || min_bound >= rank_bound)) break;
+      if (attempt == 0 ? !by_rank : !by_min || (by_rank && min_bound >= rank_bound)) continue;
       __syncthreads();
       if (tid == 0) listed = 0;
       __syncthreads();
       const float floor = of_key(bound);
+      const bool by_index = items <= NT;  // a short row is its own list (0: items that can't be drawn)
       auto put = [&](const G &g, int first) {
         float y[G::N], top = -__builtin_inff();
 #pragma unroll
@@ -681,11 +764,14 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
           y[j] = g.at(j);
           top = fmaxf(top, y[j]);
         }
-        if (bound == 1 ? top > -__builtin_inff() : top >= floor) {
+        if (by_index || (bound == 1 ? top > -__builtin_inff() : top >= floor)) {
 #pragma unroll
           for (int j = 0; j < G::N; ++j) {
             const uint32_t k = item_key(y[j]);
-            if (k >= bound) {
+            if (by_index) {
+              if (first + j < items)
+                list[first + j] = k ? static_cast<uint64_t>(k) << 32 | ~static_cast<uint32_t>(first + j) : 0ull;
+            } else if (k >= bound) {
               const int at = atomicAdd(&listed, 1);
               if (at < kCap) list[at] = static_cast<uint64_t>(k) << 32 | ~static_cast<uint32_t>(first + j);
             }
@@ -693,23 +779,17 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
         }
       };
       if constexpr (kShort) {
-        put(held, tid * G::N);
-      } else {
-        for (int first = tid * G::N; first < items; first += kAhead * NT * G::N) {
-          G g[kAhead];
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) g[u].load(x, first + u * NT * G::N, items);
-#pragma unroll
-          for (int u = 0; u < kAhead; ++u) put(g[u], first + u * NT * G::N);
+        if (tid * G::N < whole_end) put(held, tid * G::N);
+        if (has_end) {
+          G g;
+          g.load_end(x, whole_end, items);
+          put(g, whole_end);
         }
-      }
-      if (has_end) {
-        G g;
-        g.load_end(x, whole_end, items);
-        put(g, whole_end);
+      } else {
+        row.each_granule([&](int first, const G &g) { put(g, first); });
       }
       __syncthreads();
-      const int n = listed;
+      const int n = by_index ? items : listed;
       whole = n <= kCap;  // the list holds every item that reaches the bound
       if (whole && n <= NT) {
         // 3. the sorted list
@@ -717,7 +797,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
         while (size < n) size <<= 1;
         const uint64_t c = block_sort<NT, uint64_t>(tid < n ? list[tid] : 0ull, size, bins);
         const uint32_t key = static_cast<uint32_t>(c >> 32), at = ~static_cast<uint32_t>(c);
-        const bool real = tid < n;
+        const bool real = key != 0;
         const float y = real ? of_key(key) : 0.f, w = real ? sc.weight(y) : 0.f;
         float incl = w;
 #pragma unroll
@@ -736,7 +816,8 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
         }
         float mass = sum;  // what top-p is a share of
         if (flt.k > 0 && flt.p < 1.f) {
-          if (tid == min(flt.k, n) - 1) tmp[16] = __builtin_bit_cast(uint32_t, before + w);
+          // the mass of the first k, or of all there are
+          if (tid == min(flt.k, size) - 1) tmp[16] = __builtin_bit_cast(uint32_t, before + w);
           __syncthreads();
           mass = __builtin_bit_cast(float, static_cast<uint32_t>(tmp[16]));
         }
@@ -761,22 +842,18 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       } else if (whole) {
         // a longer list: it has to hold the prefix, as above
         ListItems<NT> li{list, n};
-        uint64_t all = 0;
-        li.each([&](int, uint32_t q) { all += sc.mass(of_key(q)); });
+        float all = 0.f;
+        li.each([&](int, uint32_t q) { all += sc.weight(of_key(q)); });
         all = block_sum<NT>(all, tmp);
-        const uint64_t total = static_cast<uint64_t>(sum * kMass);
-        whole = flt.k > 0 || bound == 1 || static_cast<double>(all) >= static_cast<double>(flt.p) * static_cast<double>(total) ||
-                (min_bound > 1 && bound == min_bound);
-        if (whole) drawn = select_prefix<NT>(li, sc, flt, divisor, greedy ? nullptr : noise, total, bins, tmp);
+        whole = flt.k > 0 || bound == 1 || all >= flt.p * sum || (min_bound > 1 && bound == min_bound);
+        if (whole) drawn = select_prefix<NT>(li, sc, flt, divisor, greedy ? nullptr : noise, bound == 1, bins, tmp);
       }
     }
     if (!whole) {
-      RowItems<T, NT> row{x, items};
-      const uint64_t total = static_cast<uint64_t>(sum * kMass);
       if (flt.k == 0 && flt.p == 1.f)
-        drawn = race_row<NT>(row, sc, 0, flt.min, divisor, noise, bins, tmp);
-      else if (flt.k > 0 || !select_share<NT>(row, sc, flt, divisor, noise, total, bins, list, &listed, tmp, drawn))
-        drawn = select_prefix<NT>(row, sc, flt, divisor, greedy ? nullptr : noise, total, bins, tmp);
+        drawn = race_row(row, sc, 0, flt.min, divisor, noise, bins, tmp);
+      else if (flt.k > 0 || !select_share(row, sc, flt, divisor, noise, bins, list, &listed, tmp, drawn))
+        drawn = select_prefix<NT>(row, sc, flt, divisor, greedy ? nullptr : noise, true, bins, tmp);
     }
   }
   if (tid == 0) {
