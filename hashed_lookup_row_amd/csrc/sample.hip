@@ -40,7 +40,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr float kUnits = 2147483648.f;  // 2^31
 constexpr int kBins = 2048;
-constexpr int kList = 4096;
+constexpr int kList = 6144;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kMost = 3.402823466e38f;
 
@@ -121,22 +121,35 @@ struct Granule {
   }
 };
 
-// The whole row, from memory, four granules in flight per thread.
-template <typename T, int NT>
+// The whole row: each thread's first H granules from LDS, once `fill` has put
+// them there, the others from memory, four in flight per thread.
+template <typename T, int NT, int H>
 struct RowItems {
   using G = Granule<T>;
   const T *x;
   int items;
-  template <typename F>
-  __device__ __forceinline__ void each_granule(F f) const {
+  u4 *held;  // H * NT, granule u of thread t at u * NT + t
+  template <bool kFill, typename F>
+  __device__ __forceinline__ void walk(F f) const {
     constexpr int kAhead = 4;
-    int first = threadIdx.x * G::N;
-    for (; first < items; first += kAhead * NT * G::N) {
+    int u = 0;
+    if constexpr (!kFill)
+#pragma unroll 1
+      for (; u < H && (u * NT + static_cast<int>(threadIdx.x)) * G::N < items; ++u) {
+        G g;
+        g.raw = held[u * NT + threadIdx.x];
+        f((u * NT + static_cast<int>(threadIdx.x)) * G::N, g);
+      }
+#pragma unroll 1
+    for (int first = (u * NT + static_cast<int>(threadIdx.x)) * G::N; first < items; first += kAhead * NT * G::N, u += kAhead) {
       G g[kAhead];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) g[u].load(x, first + u * NT * G::N, items);
+      for (int v = 0; v < kAhead; ++v) g[v].load(x, first + v * NT * G::N, items);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) f(first + u * NT * G::N, g[u]);
+      for (int v = 0; v < kAhead; ++v) {
+        if (kFill && u + v < H) held[(u + v) * NT + threadIdx.x] = g[v].raw;
+        f(first + v * NT * G::N, g[v]);
+      }
     }
     const int end = items / G::N * G::N;  // the granule the row ends in, if it ends within one, is one thread's
     if (threadIdx.x == NT - 1 && end < items) {
@@ -144,6 +157,14 @@ struct RowItems {
       g.load_end(x, end, items);
       f(end, g);
     }
+  }
+  template <typename F>
+  __device__ __forceinline__ void fill(F f) const {
+    walk<true>(f);
+  }
+  template <typename F>
+  __device__ __forceinline__ void each_granule(F f) const {
+    walk<false>(f);
   }
   // Scores: -inf for items that can't be drawn.
   template <typename F>
@@ -487,38 +508,33 @@ __device__ Drawn select_prefix(const Items &items, Scale sc, Filters flt, float 
   return race.key ? Drawn{race.key, race.index} : Drawn{best, first};
 }
 
-// The race over a row's kept items: those that rank at or above `last` (key and
-// complemented index) and have min-p's weight.
-template <typename T, int NT>
-__device__ Drawn race_row(const RowItems<T, NT> &row, Scale sc, uint64_t last, float least, float divisor, const float *noise,
-                          uint64_t *bins, uint64_t *tmp) {
+// The race over the items of a row that `kept(y)` says stay, and that have
+// min-p's weight; `seen(i, y)` is called for every item.  first: the lowest index of the best score.
+template <typename T, int NT, int H, typename Kept, typename Seen>
+__device__ void race_row(const RowItems<T, NT, H> &row, Scale sc, float least, float divisor, const float *noise, Race &race,
+                         uint32_t &first, Kept stays, Seen seen) {
   using G = Granule<T>;
-  const uint32_t best = key_of(sc.top), last_key = static_cast<uint32_t>(last >> 32);
-  const float lowest = of_key(max(last_key, 1u));  // of the kept scores; NaN (nothing is below it) if all are
-  uint32_t first = 0xffffffffu;
-  Race race;
   row.each_granule([&](int at, const G &g) {
-    float y[G::N], top = -__builtin_inff();
-#pragma unroll
-    for (int j = 0; j < G::N; ++j) {
-      y[j] = g.at(j);
-      top = fmaxf(top, y[j]);
-    }
-    if (!(top > -__builtin_inff()) || top < lowest || !(sc.weight(top) >= least || top == sc.top)) return;
     uint32_t kept = 0;
 #pragma unroll
     for (int j = 0; j < G::N; ++j) {
-      const uint32_t q = item_key(y[j]), i = at + j;
-      if (q == best) first = min(first, i);
-      if (q != 0 && (static_cast<uint64_t>(q) << 32 | ~i) >= last && sc.weight(y[j]) >= least) kept |= 1u << j;
+      const float y = g.at(j);
+      if (y == sc.top) first = min(first, static_cast<uint32_t>(at + j));
+      if (stays(y) && sc.weight(y) >= least) kept |= 1u << j;
+      seen(at + j, y);
     }
     while (kept) {  // few of a granule's items are kept: as many turns as the lane with the most has
-      const int j = __builtin_ctz(kept), i = at + j;
+      const int i = at + __builtin_ctz(kept);
       kept &= kept - 1;
       const float x = clean(static_cast<float>(row.x[i]));
       race.enter(x / divisor - logf(noise[i]), item_key(x), i);
     }
   });
+}
+
+// The winner, or where no score is a number the first item.
+template <int NT>
+__device__ __forceinline__ Drawn settle(Race &race, uint32_t best, uint32_t first, uint64_t *bins, uint64_t *tmp) {
   race.block_join<NT>(bins);
   if (race.key) return Drawn{race.key, race.index};
   return Drawn{best, ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp))};
@@ -526,10 +542,10 @@ __device__ Drawn race_row(const RowItems<T, NT> &row, Scale sc, uint64_t last, f
 
 // Top-p alone, for rows whose prefix is long: masses by linear bins of
 // log2 w (1/64 wide, so that few lanes meet in one; a histogram of float
-// bits has its items in a few dozen), then the items of the bin that the
-// edge lies in, sorted.  False if those are too many (equal scores).
-template <typename T, int NT>
-__device__ bool select_share(const RowItems<T, NT> &items, Scale sc, Filters flt, float divisor, const float *noise,
+// bits has its items in a few dozen); then the bins above the edge's race, while the items of the edge's
+// bin go to a list, whose kept ones, once sorted, race too.  False if those are too many (equal scores).
+template <typename T, int NT, int H>
+__device__ bool select_share(const RowItems<T, NT, H> &items, Scale sc, Filters flt, float divisor, const float *noise,
                              uint64_t *buf, uint64_t *list, int *listed, uint64_t *tmp, Drawn &drawn) {
   uint32_t *bins = reinterpret_cast<uint32_t *>(buf);
   const auto bin_of = [&](float y) {
@@ -542,13 +558,13 @@ __device__ bool select_share(const RowItems<T, NT> &items, Scale sc, Filters flt
   // All items below `far` together hold less than top-p leaves out: they can't
   // be at the edge, and are most of a long row.
   const float far = fminf(log2f(static_cast<float>(items.items) * sc.units / (kUnits * (1.f - flt.p))) + 0.01f, 1e9f);
-  uint64_t total = 0;
+  uint32_t total = 0;  // all masses together are 2^31, less or more their rounding
   items.each_score([&](int, float y) {
     const uint32_t m = sc.mass(y);  // 0 for -inf
     total += m;
     if ((sc.top - y) * sc.f < far) atomicAdd(&bins[bin_of(y)], m);
   });
-  const uint64_t goal = share_of(block_sum<NT>(total, tmp), flt.p);
+  const uint64_t goal = share_of(block_sum<NT>(static_cast<uint64_t>(total), tmp), flt.p);
   __syncthreads();
   constexpr int per = kBins / NT;
   uint64_t mine = 0;
@@ -577,12 +593,16 @@ __device__ bool select_share(const RowItems<T, NT> &items, Scale sc, Filters flt
   if (edge == bin) tmp[16] = edge_above;
   __syncthreads();
   const uint64_t above = tmp[16];
-  items.each_score([&](int i, float y) {
-    if (bin_of(y) == bin && y > -__builtin_inff()) {
-      const int at = atomicAdd(listed, 1);
-      if (at < NT) list[at] = static_cast<uint64_t>(key_of(y)) << 32 | ~static_cast<uint32_t>(i);
-    }
-  });
+  Race race;
+  uint32_t first = 0xffffffffu;
+  race_row(
+      items, sc, flt.min, divisor, noise, race, first, [&](float y) { return bin_of(y) < bin && y > -__builtin_inff(); },
+      [&](int i, float y) {
+        if (bin_of(y) == bin && y > -__builtin_inff()) {
+          const int at = atomicAdd(listed, 1);
+          if (at < NT) list[at] = static_cast<uint64_t>(key_of(y)) << 32 | ~static_cast<uint32_t>(i);
+        }
+      });
   __syncthreads();
   const int n = *listed;
   if (n > NT) return false;
@@ -602,20 +622,27 @@ __device__ bool select_share(const RowItems<T, NT> &items, Scale sc, Filters flt
   __syncthreads();
   run += above - mine;
   for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
-  // the last kept item; complemented, so that the largest is the lowest in rank
-  const uint64_t last = ~block_max<NT>(real && run < goal ? ~c : 0ull, tmp);
-  drawn = race_row(items, sc, last, flt.min, divisor, noise, buf, tmp);
+  if (real && run < goal) {
+    const float y = of_key(static_cast<uint32_t>(c >> 32));
+    const uint32_t i = ~static_cast<uint32_t>(c);
+    if (sc.weight(y) >= flt.min) race.enter(y / divisor - logf(noise[i]), static_cast<uint32_t>(c >> 32), i);
+  }
+  drawn = settle<NT>(race, key_of(sc.top), first, buf, tmp);
   return true;
 }
 
-// kShort: a granule per thread covers the row, and is held; longer rows are
-// read twice (held in registers they spilled, and the second read comes from the caches: 18
-// us instead of 22 for one row of 32,003 fp32 scores, 197 instead of 382 for 256 of 131,072 bf16).
-template <typename T, int NT, bool kShort>
+// kOne: an item per thread covers the row, and the sort takes it as it is.
+// Longer rows are read from memory once as far as LDS holds them (5 granules
+// a thread, 40,960 16-bit or 20,480 fp32 scores), and again by each later pass
+// beyond that: a second pass over 131,072 bf16 scores per CU costs 15 us from
+// memory.  Held in registers, granules spilled.
+template <typename T, int NT, bool kOne>
 __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   using G = Granule<T>;
+  constexpr int H = kOne ? 0 : 5;
   __shared__ uint64_t bins[kBins / 2 > 2 * NT ? kBins / 2 : 2 * NT];  // a histogram, or a sort's buffers
-  __shared__ uint64_t list[NT * G::N < kList ? NT * G::N : kList];
+  __shared__ uint64_t list[kOne ? 1 : kList];
+  __shared__ u4 row_held[kOne ? 1 : H * NT];
   __shared__ uint64_t tmp[17];
   __shared__ int listed;
   constexpr int kCap = sizeof(list) / 8;
@@ -649,13 +676,17 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
 #pragma unroll
     for (int j = 0; j < G::N; ++j) sum += __builtin_amdgcn_exp2f((y[j] - ref) * f);
   };
-  // the granule the row ends in, if it ends within one, is one thread's
-  const int whole_end = items / G::N * G::N;
-  const bool has_end = tid == NT - 1 && whole_end < items;
-  const RowItems<T, NT> row{x, items};
+  const RowItems<T, NT, H> row{x, items, row_held};
   Race race;
-  G held;
-  if (open) {
+  uint64_t own = 0;  // kOne: this thread's item, as a list has it
+  if constexpr (kOne) {
+    const float y = tid < items ? clean(static_cast<float>(x[tid])) : -__builtin_inff();
+    mine = y;
+    ref = fmaxf(ref, y);
+    sum = __builtin_amdgcn_exp2f((y - ref) * f);
+    if (item_key(y) != 0) own = static_cast<uint64_t>(key_of(y)) << 32 | ~static_cast<uint32_t>(tid);
+    if (open && own != 0) race.enter(y / divisor - logf(noise[tid]), key_of(y), tid);
+  } else if (open) {
     for (int first = tid * G::N; first < items; first += NT * G::N) {
       G g;
       float e[G::N];
@@ -674,16 +705,8 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
         if (y > -__builtin_inff()) race.enter(y / divisor - logf(e[j]), key_of(y), first + j);
       }
     }
-  } else if constexpr (kShort) {
-    held.load(x, tid * G::N, items);
-    take(held);
   } else {
-    row.each_granule([&](int, const G &g) { take(g); });
-  }
-  if (kShort && !open && has_end) {
-    G g;
-    g.load_end(x, whole_end, items);
-    take(g);
+    row.fill([&](int, const G &g) { take(g); });
   }
   const uint32_t best = static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(item_key(mine)), tmp));
   if (best == 0) {
@@ -701,17 +724,17 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
     race.block_join<NT>(bins);
     drawn = Drawn{race.key, race.index};
     if (race.key == 0) {  // no score is a number (the noise is not): the first item
-      uint32_t first = 0xffffffffu;
-      row.each([&](int i, uint32_t q) {
-        if (q == best) first = min(first, static_cast<uint32_t>(i));
-      });
+      uint32_t first = own >> 32 == best ? static_cast<uint32_t>(tid) : 0xffffffffu;
+      if constexpr (!kOne)
+        for (int i = tid; i < items; i += NT)
+          if (item_key(clean(static_cast<float>(x[i]))) == best) first = min(first, static_cast<uint32_t>(i));
       drawn = Drawn{best, ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp))};
     }
   } else {
     // 2. the bound, and the list of the items that reach it
     uint32_t rank_bound = 1, min_bound = 1;
     bool by_rank = true, by_min = false;  // which bounds are worth a list
-    if (items > NT) {
+    if constexpr (!kOne) {
       const int owners = min(NT, items / G::N);
       const int rank = flt.k > 0 ? flt.k : owners / 2;
       if (rank <= owners && (flt.k > 0 || flt.p < 1.f)) {
@@ -741,9 +764,9 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       // a little below min-p's own bound (its test follows per item); top-p's share of the first k needs all of those
       if (flt.min > 0.f && !(flt.k > 0 && flt.p < 1.f)) {
         min_bound = max(min(item_key(clean(sc.top + (log2f(flt.min) - 0.01f) / f)), best), 1u);
-        // the list overflows (4,096 items) where nearly every thread's maximum reaches the bound
+        // the list overflows (6,144 items) where nearly every thread's maximum reaches the bound
         const uint64_t reach = block_sum<NT>(static_cast<uint64_t>(item_key(mine) >= min_bound), tmp);
-        by_min = static_cast<int>(reach) * 64 <= owners * 63;
+        by_min = static_cast<int>(reach) * 256 <= owners * 255;
       }
       if (flt.k == 0 && flt.p == 1.f) by_rank = false;
     }
@@ -756,46 +779,33 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       if (tid == 0) listed = 0;
       __syncthreads();
       const float floor = of_key(bound);
-      const bool by_index = items <= NT;  // a short row is its own list (0: items that can't be drawn)
-      auto put = [&](const G &g, int first) {
-        float y[G::N], top = -__builtin_inff();
-#pragma unroll
-        for (int j = 0; j < G::N; ++j) {
-          y[j] = g.at(j);
-          top = fmaxf(top, y[j]);
-        }
-        if (by_index || (bound == 1 ? top > -__builtin_inff() : top >= floor)) {
+      if constexpr (!kOne)
+        row.each_granule([&](int first, const G &g) {
+          float y[G::N], top = -__builtin_inff();
 #pragma unroll
           for (int j = 0; j < G::N; ++j) {
-            const uint32_t k = item_key(y[j]);
-            if (by_index) {
-              if (first + j < items)
-                list[first + j] = k ? static_cast<uint64_t>(k) << 32 | ~static_cast<uint32_t>(first + j) : 0ull;
-            } else if (k >= bound) {
-              const int at = atomicAdd(&listed, 1);
-              if (at < kCap) list[at] = static_cast<uint64_t>(k) << 32 | ~static_cast<uint32_t>(first + j);
+            y[j] = g.at(j);
+            top = fmaxf(top, y[j]);
+          }
+          if (bound == 1 ? top > -__builtin_inff() : top >= floor) {
+#pragma unroll
+            for (int j = 0; j < G::N; ++j) {
+              const uint32_t k = item_key(y[j]);
+              if (k >= bound) {
+                const int at = atomicAdd(&listed, 1);
+                if (at < kCap) list[at] = static_cast<uint64_t>(k) << 32 | ~static_cast<uint32_t>(first + j);
+              }
             }
           }
-        }
-      };
-      if constexpr (kShort) {
-        if (tid * G::N < whole_end) put(held, tid * G::N);
-        if (has_end) {
-          G g;
-          g.load_end(x, whole_end, items);
-          put(g, whole_end);
-        }
-      } else {
-        row.each_granule([&](int first, const G &g) { put(g, first); });
-      }
+        });
       __syncthreads();
-      const int n = by_index ? items : listed;
-      whole = n <= kCap;  // the list holds every item that reaches the bound
+      const int n = kOne ? items : listed;
+      whole = kOne || n <= kCap;  // the list holds every item that reaches the bound
       if (whole && n <= NT) {
         // 3. the sorted list
         int size = kWave;
         while (size < n) size <<= 1;
-        const uint64_t c = block_sort<NT, uint64_t>(tid < n ? list[tid] : 0ull, size, bins);
+        const uint64_t c = block_sort<NT, uint64_t>(kOne ? own : tid < n ? list[tid] : 0ull, size, bins);
         const uint32_t key = static_cast<uint32_t>(c >> 32), at = ~static_cast<uint32_t>(c);
         const bool real = key != 0;
         const float y = real ? of_key(key) : 0.f, w = real ? sc.weight(y) : 0.f;
@@ -839,7 +849,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
           __syncthreads();
           drawn = Drawn{static_cast<uint32_t>(tmp[16] >> 32), ~static_cast<uint32_t>(tmp[16])};
         }
-      } else if (whole) {
+      } else if (!kOne && whole) {
         // a longer list: it has to hold the prefix, as above
         ListItems<NT> li{list, n};
         float all = 0.f;
@@ -849,12 +859,15 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
         if (whole) drawn = select_prefix<NT>(li, sc, flt, divisor, greedy ? nullptr : noise, bound == 1, bins, tmp);
       }
     }
-    if (!whole) {
-      if (flt.k == 0 && flt.p == 1.f)
-        drawn = race_row(row, sc, 0, flt.min, divisor, noise, bins, tmp);
-      else if (flt.k > 0 || !select_share(row, sc, flt, divisor, noise, bins, list, &listed, tmp, drawn))
-        drawn = select_prefix<NT>(row, sc, flt, divisor, greedy ? nullptr : noise, true, bins, tmp);
-    }
+    if constexpr (!kOne)
+      if (!whole) {
+        if (flt.k == 0 && flt.p == 1.f) {
+          uint32_t first = 0xffffffffu;
+          race_row(row, sc, flt.min, divisor, noise, race, first, [](float y) { return y > -__builtin_inff(); }, [](int, float) {});
+          drawn = settle<NT>(race, best, first, bins, tmp);
+        } else if (flt.k > 0 || !select_share(row, sc, flt, divisor, noise, bins, list, &listed, tmp, drawn))
+          drawn = select_prefix<NT>(row, sc, flt, divisor, greedy ? nullptr : noise, true, bins, tmp);
+      }
   }
   if (tid == 0) {
     a.index[r] = drawn.index;
@@ -862,15 +875,13 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   }
 }
 
-// Threads by the row's length: one item per thread of a sort where the row is
-// that short.
+// Threads by the row's length: one item per thread where the row is that short.
 template <typename T>
 void launch(const SampleArgs &a, int64_t rows, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(rows);
-  constexpr int N = Granule<T>::N;
   if (a.items <= 256)
     sample_kernel<T, 256, true><<<grid, 256, 0, stream>>>(a);
-  else if (a.items <= 1024 * N)
+  else if (a.items <= 1024)
     sample_kernel<T, 1024, true><<<grid, 1024, 0, stream>>>(a);
   else
     sample_kernel<T, 1024, false><<<grid, 1024, 0, stream>>>(a);
