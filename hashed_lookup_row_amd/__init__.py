@@ -9,6 +9,7 @@ is not on a GPU, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -37,6 +38,8 @@ class HLRError(RuntimeError):
 def load_library():
     """Loads libhlr.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -124,6 +127,8 @@ def _check(rc: int, what: str):
 
 
 def _dev(t: torch.Tensor, name: str, dtype=None):
+    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.device.type != "cuda":
@@ -714,9 +719,8 @@ def hist_plan(cached, new, block_table, free_blocks, block, max_tokens, out=None
     if new.numel() != n or block_table.dim() != 2 or block_table.shape[0] != n:
         raise HLRError("cached, new and block_table must have one entry (row) per request")
     if out is None:
-        out = (torch.empty(int(max_tokens), dtype=torch.int64, device=dev),
-               torch.empty(n + 1, dtype=torch.int32, device=dev), torch.empty(n, dtype=torch.int32, device=dev),
-               torch.empty(2, dtype=torch.int64, device=dev))
+        out = (torch.empty(int(max_tokens), dtype=torch.int64, device=dev), cached.new_empty(n + 1),
+               cached.new_empty(n), torch.empty(2, dtype=torch.int64, device=dev))
     else:
         for t, name, dt, size in zip(out, ("slots", "cu", "lengths", "counts"),
                                      (torch.int64, torch.int32, torch.int32, torch.int64), (max_tokens, n + 1, n, 2)):
@@ -766,6 +770,7 @@ def hist_read(k_codes, v_codes, k_scale, v_scale, slots, dtype=torch.float32, ou
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
 def hist_attention_workspace_size(tokens, requests, q_heads, kv_heads, dim, max_q, max_len) -> int:
     return int(load_library().hist_attention_workspace_size(int(tokens), int(requests), int(q_heads), int(kv_heads),
                                                             int(dim), int(max_q), int(max_len)))
@@ -789,13 +794,13 @@ def hist_attention(q, k_codes, v_codes, k_scale, v_scale, block_table, lengths, 
         raise HLRError("block_table must have a row per request, and cu one entry more than requests")
     dev = q.device
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=dev)
+        out = q.new_empty((tokens, heads, dim))
     else:
         _dev(out, "out", q.dtype)
         if out.numel() != q.numel():
             raise HLRError("out must hold tokens x heads x dim values")
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
-    need = lib.hist_attention_workspace_size(tokens, n, heads, kv_heads, dim, max_q, max_len)
+    lse = k_scale.new_empty((tokens, heads)) if return_lse else None
+    need = hist_attention_workspace_size(tokens, n, heads, kv_heads, dim, max_q, max_len)
     if need == 0:
         w, wb = None, 0
     elif ws is not None:
@@ -838,9 +843,10 @@ def sample_scores(scores, noise, temperature=None, top_k=None, top_p=None, min_p
         raise HLRError("noise must be float32 of the scores' shape")
     rows, items = scores.shape
     dev = scores.device
-    index, logprob = out if out is not None else (torch.empty(rows, dtype=torch.int64, device=dev),
-                                                  torch.empty(rows, dtype=torch.float32, device=dev))
-    if out is not None:
+    if out is None:
+        index, logprob = torch.empty(rows, dtype=torch.int64, device=dev), noise.new_empty(rows)
+    else:
+        index, logprob = out
         _per_row(index, "out index", torch.int64, rows)
         _per_row(logprob, "out logprob", torch.float32, rows)
     _check(lib.sample_scores(scores.data_ptr(), code, rows, items, scores.stride(0), noise.data_ptr(), noise.stride(0),

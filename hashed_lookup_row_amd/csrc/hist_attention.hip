@@ -95,6 +95,21 @@ __device__ __forceinline__ float lse_of(float m, float l) {
   return l == 0.f ? -__builtin_inff() : __builtin_fmaf(m, 0.693147180559945309f, logf(ldexpf(l, -static_cast<int>(kUp))));
 }
 
+// A tile of 64 tokens as f16 in LDS, in units of 16 bytes: keys as rows (t, m)
+// of D/8 units, token(t, m) as above; values as rows d of 8 units (unit 2 g + u:
+// tokens 8 u .. 8 u + 7 of chunk g).  A read takes one unit of 16
+// successive rows; the units of a row are permuted (xor) so that any eight of
+// those lie in different banks.
+template <int D>
+struct RowTile {
+  static constexpr int kUnits = D / 8, kKeys = 64 * kUnits, kValues = D * 8;  // units of a key row, of both tiles
+  static __device__ __forceinline__ int key_at(int t, int m, int unit) {
+    const int by = kUnits >= 8 ? m & (kUnits - 1) : m >> 1 & (kUnits - 1);
+    return (t * 16 + m) * kUnits + (unit ^ by);
+  }
+  static __device__ __forceinline__ int value_at(int d, int unit) { return d * 8 + (unit ^ (d & 7)); }
+};
+
 // One wave's state for NQ tiles of 16 rows.
 template <typename T, int D, int NQ>
 struct Wave {
@@ -186,6 +201,42 @@ struct Wave {
     }
   }
 
+  // The products from f16 tiles in LDS (RowTile below), K's rows in the order
+  // of the A operand.
+  __device__ __forceinline__ void scores(const u4 *kt, f4 (&s)[NQ][4]) const {
+    const int lane = lane_id(), n = lane % 16, g = lane / 16;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int x = 0; x < NQ; ++x) s[x][t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int unit = D >= 64 ? (c / 2) * 8 + 2 * g + c % 2 : g;
+        const h8 kf = __builtin_bit_cast(h8, kt[RowTile<D>::key_at(t, n, unit)]);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) s[x][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[x][p][c], s[x][t], 0, 0, 0);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void values(const u4 *vt, const f4 (&s)[NQ][4]) {
+    const int lane = lane_id(), n = lane % 16, g = lane / 16;
+    h8 p[NQ][NW][2];
+    weights16(s, p);
+#pragma unroll
+    for (int e = 0; e < ND; ++e)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const h8 vf = __builtin_bit_cast(h8, vt[RowTile<D>::value_at(e * 16 + n, 2 * g + u)]);
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+#pragma unroll
+          for (int k = 0; k < NW; ++k) acc[x][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[x][k][u], acc[x][e], 0, 0, 0);
+      }
+  }
+
   // Masks the scores, keeps the running maxima (m of the scores, m2 of the scores times the value scales, both in
   // log2 and whole numbers, so every rescaling is exact), adds up l and leaves the weights times the value scales in
   // s.  Maxima are compared per lane and joined over the lane groups only when some lane passes them by kSlack; a row
@@ -246,8 +297,8 @@ struct Wave {
     }
   }
 
-  __device__ __forceinline__ void values(const u4 (&vr)[ND], const f4 (&s)[NQ][4]) {
-    h8 p[NQ][NW][2];
+  // The B operand of the second product: the weights as f16, in one part or two.
+  __device__ __forceinline__ void weights16(const f4 (&s)[NQ][4], h8 (&p)[NQ][NW][2]) const {
 #pragma unroll
     for (int x = 0; x < NQ; ++x)
 #pragma unroll
@@ -261,6 +312,11 @@ struct Wave {
           p[x][0][u][j] = static_cast<_Float16>(y);
           if constexpr (NW == 2) p[x][1][u][j] = static_cast<_Float16>(y - static_cast<float>(p[x][0][u][j]));
         }
+  }
+
+  __device__ __forceinline__ void values(const u4 (&vr)[ND], const f4 (&s)[NQ][4]) {
+    h8 p[NQ][NW][2];
+    weights16(s, p);
 #pragma unroll
     for (int e = 0; e < ND; ++e)
 #pragma unroll
@@ -332,8 +388,165 @@ __device__ __forceinline__ int length_of(const Args &a, int r) {
   return max(0, static_cast<int>(min(static_cast<int64_t>(a.lengths[r]), most)));
 }
 
+// Rows' results, from a wave: to the output, or to a split's part.
+template <typename T, int D, int NQ>
+__device__ __forceinline__ void store_rows(const Args &a, Wave<T, D, NQ> &w, int kvh, int first, int row0, int rows, int split) {
+  const int lane = lane_id(), n = lane % 16, g = lane / 16, heads = a.kv_heads * a.group;
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    const int row = row0 + 16 * x + n;
+    if (row >= rows) continue;
+    const int64_t at = static_cast<int64_t>(first + row / a.group) * heads + kvh * a.group + row % a.group;
+    const float inv = w.l[x] > 0.f ? 1.f / w.l[x] : (w.l[x] == 0.f ? 0.f : w.l[x]);  // a row that sees nothing: zeros
+    const float f = inv * pow2(w.m2[x] - w.m[x]);
+    if (a.part) {
+      const int64_t to = static_cast<int64_t>(split) * a.tokens * heads + at;
+      if (g == 0) a.part_ml[to] = make_float2(w.m[x], w.l[x]);
+#pragma unroll
+      for (int e = 0; e < w.ND; ++e) *reinterpret_cast<f4 *>(a.part + to * D + e * 16 + 4 * g) = w.acc[x][e] * f;
+    } else {
+      T *o = static_cast<T *>(a.out) + at * D;
+      if (g == 0 && a.lse) a.lse[at] = lse_of(w.m[x], w.l[x]);
+#pragma unroll
+      for (int e = 0; e < w.ND; ++e) {
+        T y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = static_cast<T>(w.acc[x][e][i] * f);
+        __builtin_memcpy(__builtin_assume_aligned(o + e * 16 + 4 * g, 4 * sizeof(T)), y, sizeof(y));
+      }
+    }
+  }
+}
+
+// Many rows: each of the four waves has 16 NQ of them and all walk the same
+// tiles.  A tile is fetched and turned into f16 once per block, a quarter by
+// each wave, into one of two LDS buffers: while a tile is worked on, the codes of
+// the next are in flight to registers, and go to the other buffer between its two products.
+template <typename T, int D, int NQ>
+__global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) rows_kernel(Args a) {
+  using W = Wave<T, D, NQ>;
+  using R = RowTile<D>;
+  constexpr int NT = kWaves * kWave, kPieces = 64 * D / 16 / NT;  // 16-byte pieces of keys (and of values) per thread
+  static_assert(D >= 64, "a thread has a piece");
+  __shared__ u4 buf[2][R::kKeys + R::kValues];
+  const int tid = threadIdx.x, lane = lane_id(), g = lane / 16;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int split = blockIdx.x / a.row_tiles, rt = a.row_tiles - 1 - blockIdx.x % a.row_tiles;
+  const int kvh = blockIdx.y, r = blockIdx.z;
+  const int first = a.cu[r], fresh = min(a.cu[r + 1], static_cast<int>(a.tokens)) - first;
+  const int rows = min(fresh, a.max_q) * a.group;
+  const int block_row0 = rt * kWaves * 16 * NQ, row0 = block_row0 + wave * 16 * NQ;
+  if (first < 0 || fresh <= 0 || block_row0 >= rows) return;
+  const int length = length_of(a, r);
+  const int64_t split_lo = static_cast<int64_t>(split) * a.chunk;
+  if (split > 0 && split_lo >= length) return;  // the combine knows that this split is empty
+
+  W w;
+  w.load_queries(a, r, kvh, min(row0, rows), rows, first, fresh, length);
+  const int *table = a.table + r * a.cols;
+
+  // positions that rows [b, e) see any of
+  const auto span = [&](int b, int e, int &lo, int &hi) {
+    lo = 0;
+    hi = b < e ? length : 0;
+    if (a.causal && b < e) {
+      hi = min(length, max(0, length - fresh + (e - 1) / a.group + 1));
+      if (a.window > 0) lo = max(0, length - fresh + b / a.group + 1 - a.window);
+    }
+    if (a.part) {
+      lo = max(lo, static_cast<int>(split_lo));
+      hi = static_cast<int>(min(static_cast<int64_t>(hi), split_lo + a.chunk));
+    }
+  };
+  int lo, hi, my_lo, my_hi;
+  span(block_row0, min(block_row0 + kWaves * 16 * NQ, rows), lo, hi);
+  span(row0, min(row0 + 16 * NQ, rows), my_lo, my_hi);
+  const int tile_lo = lo / kTile, tile_hi = hi > lo ? (hi + kTile - 1) / kTile : 0;
+
+  u4 kr[kPieces], vr[kPieces];
+  int id_k[kPieces], id_v[kPieces];
+  const int in_b = (1 << a.log_b) - 1;
+  // key piece i: 16 elements of token (i * NT + tid) / (D / 16); value piece: chunk (i * NT + tid) / D, one element
+  const auto ids = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = i * NT + tid;
+      id_k[i] = max(block_of(a, table, tile * kTile + piece / (D / 16)), 0);
+      id_v[i] = max(block_of(a, table, tile * kTile + piece / D * 16), 0);
+    }
+  };
+  const auto fetch = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = i * NT + tid, token = piece / (D / 16), chunk = piece / D;
+      const int64_t kb = (static_cast<int64_t>(id_k[i]) * a.kv_heads + kvh) << a.log_b;
+      const int64_t vb = (static_cast<int64_t>(id_v[i]) * a.kv_heads + kvh) << (a.log_b - 4);
+      kr[i] = *reinterpret_cast<const u4 *>(a.k + (kb + ((tile * kTile + token) & in_b)) * D + piece % (D / 16) * 16);
+      vr[i] = *reinterpret_cast<const u4 *>(a.v + ((vb + (((tile * kTile + chunk * 16) & in_b) >> 4)) * D + piece % D) * 16);
+    }
+  };
+  const auto convert = [&](u4 *to) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = i * NT + tid, token = piece / (D / 16), unit = piece % (D / 16) * 2;
+      const int t = token % 16 / 4, m = token / 16 * 4 + token % 4;
+      to[R::key_at(t, m, unit)] = __builtin_bit_cast(u4, f16_of_codes(kr[i][0], kr[i][1]));
+      to[R::key_at(t, m, unit + 1)] = __builtin_bit_cast(u4, f16_of_codes(kr[i][2], kr[i][3]));
+      const int chunk = piece / D, d = piece % D;
+      to[R::kKeys + R::value_at(d, 2 * chunk)] = __builtin_bit_cast(u4, f16_of_codes(vr[i][0], vr[i][1]));
+      to[R::kKeys + R::value_at(d, 2 * chunk + 1)] = __builtin_bit_cast(u4, f16_of_codes(vr[i][2], vr[i][3]));
+    }
+  };
+  // the scales of this lane's chunk
+  const auto scales = [&](int tile, int &own, float &ks, float &vs) {
+    own = block_of(a, table, tile * kTile + 16 * g);
+    const int64_t bh = static_cast<int64_t>(max(own, 0)) * a.kv_heads + kvh;
+    ks = a.ks[bh];
+    vs = a.vs[bh];
+  };
+
+  if (tile_lo < tile_hi) {
+    ids(tile_lo);
+    fetch(tile_lo);
+    int own, next_own = -1;
+    float ks, vs, next_ks = 0.f, next_vs = 0.f;
+    scales(tile_lo, own, ks, vs);
+    convert(buf[0]);
+    if (tile_lo + 1 < tile_hi) {
+      ids(tile_lo + 1);
+      fetch(tile_lo + 1);
+    }
+    __syncthreads();
+    for (int tile = tile_lo; tile < tile_hi; ++tile) {
+      const u4 *now = buf[(tile - tile_lo) & 1];
+      const bool more = tile + 1 < tile_hi;
+      const bool mine = tile * kTile < my_hi && (tile + 1) * kTile > my_lo;
+      if (more) scales(tile + 1, next_own, next_ks, next_vs);
+      if (tile + 2 < tile_hi) ids(tile + 2);
+      f4 s[NQ][4];
+      if (mine) {
+        w.scores(now, s);
+        w.weights(s, ks, vs, own >= 0, tile * kTile);
+      }
+      if (more) convert(buf[(tile + 1 - tile_lo) & 1]);
+      if (tile + 2 < tile_hi) fetch(tile + 2);
+      if (mine) w.values(now + R::kKeys, s);
+      own = next_own;
+      ks = next_ks;
+      vs = next_vs;
+      __syncthreads();
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < NQ; ++x) {
+    w.l[x] += xor16(w.l[x]);
+    w.l[x] += xor32(w.l[x]);
+  }
+  store_rows(a, w, kvh, first, row0, rows, split);
+}
+
 // kKeys: the four waves of a block share its rows and take its tiles in turn
-// (few rows, long histories); otherwise each wave has its own rows and all
+// (few rows, long histories); otherwise (D = 32) each wave has its own rows and all
 // walk the same tiles.
 template <typename T, int D, int NQ, bool kKeys>
 __global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
@@ -449,28 +662,7 @@ __global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
     for (int x = 0; x < NQ; ++x) w.l[x] = jl[0][x * 16 + n] + jl[1][x * 16 + n] + jl[2][x * 16 + n] + jl[3][x * 16 + n];
   }
 
-  const int heads = a.kv_heads * a.group;
-#pragma unroll
-  for (int x = 0; x < NQ; ++x) {
-    const int row = row0 + 16 * x + n;
-    if (row >= rows) continue;
-    const int64_t at = static_cast<int64_t>(first + row / a.group) * heads + kvh * a.group + row % a.group;
-    const float inv = w.l[x] > 0.f ? 1.f / w.l[x] : (w.l[x] == 0.f ? 0.f : w.l[x]);  // a row that sees nothing: zeros
-    const float f = inv * pow2(w.m2[x] - w.m[x]);
-    if (splits) {
-      const int64_t to = static_cast<int64_t>(split) * a.tokens * heads + at;
-      if (g == 0) a.part_ml[to] = make_float2(w.m[x], w.l[x]);
-#pragma unroll
-      for (int e = 0; e < W::ND; ++e) *reinterpret_cast<f4 *>(a.part + to * D + e * 16 + 4 * g) = w.acc[x][e] * f;
-    } else {
-      T *o = static_cast<T *>(a.out) + at * D;
-      if (g == 0 && a.lse) a.lse[at] = lse_of(w.m[x], w.l[x]);
-#pragma unroll
-      for (int e = 0; e < W::ND; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[e * 16 + 4 * g + i] = static_cast<T>(w.acc[x][e][i] * f);
-    }
-  }
+  store_rows(a, w, kvh, first, row0, rows, split);
 }
 
 // Joins the splits of each (token, head), one block per row: the threads' first
@@ -546,11 +738,14 @@ struct Plan {
   int nq, row_tiles, splits, chunk;
 };
 
-Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t max_q, int64_t max_len) {
+// 16-row tiles of a wave where it has rows of its own.
+constexpr int row_tiles_of(int dim) { return dim == 256 ? 1 : 2; }
+
+Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t dim, int64_t max_q, int64_t max_len) {
   Plan p{};
   const int64_t rows = max_q * group;
   p.keys = rows <= 16;
-  p.nq = p.keys ? 1 : 2;
+  p.nq = p.keys ? 1 : row_tiles_of(static_cast<int>(dim));
   const int64_t per = p.keys ? 16 : 16 * p.nq * kWaves;
   p.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t blocks = requests * kv_heads * p.row_tiles;
@@ -576,8 +771,10 @@ hlr_status launch(const Args &a, const Plan &p, int64_t requests, hipStream_t st
                   static_cast<unsigned>(requests));
   if (p.keys)
     attention_kernel<T, D, 1, true><<<grid, kWaves * kWave, 0, stream>>>(a);
+  else if constexpr (D == 32)
+    attention_kernel<T, D, row_tiles_of(D), false><<<grid, kWaves * kWave, 0, stream>>>(a);
   else
-    attention_kernel<T, D, 2, false><<<grid, kWaves * kWave, 0, stream>>>(a);
+    rows_kernel<T, D, row_tiles_of(D)><<<grid, kWaves * kWave, 0, stream>>>(a);
   if (p.splits > 1) {
     const hlr_status st = launch_status();
     if (st != HLR_OK) return st;
@@ -609,7 +806,7 @@ bool sizes_ok(int64_t tokens, int64_t requests, int64_t q_heads, int64_t kv_head
 extern "C" size_t hist_attention_workspace_size(int64_t tokens, int64_t requests, int64_t q_heads, int64_t kv_heads,
                                                 int64_t dim, int64_t max_q, int64_t max_len) {
   if (!sizes_ok(tokens, requests, q_heads, kv_heads, dim, max_q, max_len)) return 0;
-  const Plan p = plan(requests, kv_heads, q_heads / kv_heads, max_q, max_len);
+  const Plan p = plan(requests, kv_heads, q_heads / kv_heads, dim, max_q, max_len);
   if (p.splits <= 1) return 0;
   const size_t rows = static_cast<size_t>(p.splits) * tokens * q_heads;
   return round_up(rows * dim * 4, 256) + round_up(rows * 8, 256);
@@ -639,7 +836,7 @@ extern "C" hlr_status hist_attention(const void *q, int32_t type, int64_t tokens
       !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) ||
       !aligned(lengths, 4) || !aligned(cu, 4) || !aligned(out_lse, 4))
     return HLR_MISALIGNED;
-  const Plan p = plan(requests, kv_heads, q_heads / kv_heads, max_q, max_len);
+  const Plan p = plan(requests, kv_heads, q_heads / kv_heads, dim, max_q, max_len);
   Args a{};
   a.q = q;
   a.q_tok = q_token_stride;
