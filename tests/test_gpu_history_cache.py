@@ -1,0 +1,110 @@
+"""HistoryCache against the entry points it is made of and 64-bit attention, and the serving example end to end."""
+import importlib.util
+import os
+
+import pytest
+import torch
+
+import hashed_lookup_row_amd as hlr
+from hashed_lookup_row_amd.history import HistoryCache
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    hlr.load_library()
+    return torch.device("cuda:0")
+
+
+def attention64(q, k, v, hidden):
+    """q [n, H, D], k, v [m, heads, D], hidden [n, m] or None; 64 bits."""
+    group = q.shape[1] // k.shape[1]
+    out = torch.zeros(q.shape, dtype=torch.float64)
+    for h in range(q.shape[1]):
+        s = q[:, h].double().cpu() @ k[:, h // group].double().cpu().T * q.shape[2] ** -0.5
+        if hidden is not None:
+            s = s.masked_fill(hidden, float("-inf"))
+        out[:, h] = torch.softmax(s, 1) @ v[:, h // group].double().cpu()
+    return out
+
+
+@pytest.mark.parametrize("side_stream", [False, True])
+def test_histories_grow_are_attended_and_released(dev, side_stream):
+    stream = torch.cuda.Stream(dev) if side_stream else None
+    users, heads, D, B = 5, 2, 64, 16
+    cache = HistoryCache(users, 40, heads, D, 150, dev, block=B, stream=stream)
+    g = torch.Generator(device=dev)
+    g.manual_seed(1)
+    on = torch.cuda.stream(stream) if side_stream else torch.cuda.stream(torch.cuda.current_stream(dev))
+    with on:
+        for step, new in enumerate([[30, 1, 0, 17, 64], [1, 1, 1, 1, 1], [0, 40, 3, 0, 2], [1, 0, 0, 0, 0]]):
+            if step == 2:
+                cache.release(4)
+                assert cache.held == [31, 2, 1, 18, 0]
+            n = sum(new)
+            qkv = torch.randn((n, 3, 4, D), generator=g, device=dev)
+            cache.append(qkv[:, 1, :heads], qkv[:, 2, :heads], new)
+            out = cache.attend(qkv[:, 0])
+            torch.cuda.synchronize()
+            assert cache.lengths.tolist() == cache.held
+            for u in range(users):
+                assert cache.table[u, :len(cache.blocks[u])].tolist() == cache.blocks[u]
+            assert sorted(cache._free + sum(cache.blocks, [])) == list(range(40))  # no block is lost or held twice
+            at = 0
+            for u, m in enumerate(new):
+                if m:
+                    k, v = cache.read(u)
+                    pos = torch.arange(len(k))
+                    hidden = pos[None] > (len(k) - m + torch.arange(m))[:, None]
+                    want = attention64(qkv[at:at + m, 0], k, v, hidden)
+                    # fp32: values of about 1, scores below 16 in log2: (8 + 4 * 16) 2^-23 of sums of |v| < 8
+                    assert float((out[at:at + m].double().cpu() - want).abs().max()) < 72 * 2.0 ** -23 * 8
+                at += m
+        q = torch.randn((10, 4, D), generator=g, device=dev)
+        out = cache.attend(q, counts=[4, 0, 5, 1, 0])
+        torch.cuda.synchronize()
+        for u, lo, hi in ((0, 0, 4), (2, 4, 9), (3, 9, 10)):
+            k, v = cache.read(u)
+            want = attention64(q[lo:hi], k, v, None)
+            assert float((out[lo:hi].double().cpu() - want).abs().max()) < 72 * 2.0 ** -23 * 8
+
+
+def test_refusals(dev):
+    with pytest.raises(hlr.HLRError):
+        HistoryCache(2, 4, 1, 64, 100, dev, block=20)
+    with pytest.raises(hlr.HLRError):
+        HistoryCache(2, 4, 1, 48, 100, dev)
+    with pytest.raises(TypeError):
+        HistoryCache(2, 4, 1, 64, 100, dev, stream=0)
+    cache = HistoryCache(2, 4, 1, 64, 100, dev, block=16)
+    kv = torch.zeros((70, 1, 64), device=dev)
+    with pytest.raises(hlr.HLRError):
+        cache.append(kv, kv, [70])          # a count per user
+    with pytest.raises(hlr.HLRError):
+        cache.append(kv, kv, [70, 1])       # 71 events
+    with pytest.raises(hlr.HLRError):
+        cache.append(kv, kv, [70, 0])       # five blocks of four
+    with pytest.raises(hlr.HLRError):
+        cache.append(torch.zeros((101, 1, 64), device=dev), torch.zeros((101, 1, 64), device=dev), [101, 0])
+    odd = torch.zeros(64 * 64 + 1, device=dev)[1:].view(64, 1, 64)
+    with pytest.raises(hlr.HLRError):
+        cache.append(odd, odd, [64, 0])     # not 16-byte aligned: nothing is held afterwards
+    assert cache.held == [0, 0] and cache.free_blocks == 4 and cache.lengths.tolist() == [0, 0]
+    cache.append(kv[:64], kv[:64], [64, 0])
+    assert cache.free_blocks == 0
+    with pytest.raises(hlr.HLRError):
+        cache.attend(kv[:3])
+
+
+def test_serving_example(dev, capsys):
+    spec = importlib.util.spec_from_file_location("history_serving", os.path.join(ROOT, "examples", "history_serving.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    last, logprob = example.main(["--users", "7", "--items", "3000", "--candidates", "50", "--history", "90", "--steps", "4"])
+    assert "us a step" in capsys.readouterr().out
+    assert last.shape == (7,) and bool((last > 0).all())
+    assert bool((logprob <= 0).all()) and bool(torch.isfinite(logprob).all())
