@@ -121,35 +121,22 @@ struct Granule {
   }
 };
 
-// The whole row: each thread's first H granules from LDS, once `fill` has put
-// them there, the others from memory, four in flight per thread.
-template <typename T, int NT, int H>
+// The whole row, from memory, two granules in flight per thread (four take as long or longer).
+template <typename T, int NT>
 struct RowItems {
   using G = Granule<T>;
   const T *x;
   int items;
-  u4 *held;  // H * NT, granule u of thread t at u * NT + t
-  template <bool kFill, typename F>
-  __device__ __forceinline__ void walk(F f) const {
-    constexpr int kAhead = 4;
-    int u = 0;
-    if constexpr (!kFill)
+  template <typename F>
+  __device__ __forceinline__ void each_granule(F f) const {
+    constexpr int kAhead = 2;
 #pragma unroll 1
-      for (; u < H && (u * NT + static_cast<int>(threadIdx.x)) * G::N < items; ++u) {
-        G g;
-        g.raw = held[u * NT + threadIdx.x];
-        f((u * NT + static_cast<int>(threadIdx.x)) * G::N, g);
-      }
-#pragma unroll 1
-    for (int first = (u * NT + static_cast<int>(threadIdx.x)) * G::N; first < items; first += kAhead * NT * G::N, u += kAhead) {
+    for (int first = threadIdx.x * G::N; first < items; first += kAhead * NT * G::N) {
       G g[kAhead];
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) g[v].load(x, first + v * NT * G::N, items);
 #pragma unroll
-      for (int v = 0; v < kAhead; ++v) {
-        if (kFill && u + v < H) held[(u + v) * NT + threadIdx.x] = g[v].raw;
-        f(first + v * NT * G::N, g[v]);
-      }
+      for (int v = 0; v < kAhead; ++v) f(first + v * NT * G::N, g[v]);
     }
     const int end = items / G::N * G::N;  // the granule the row ends in, if it ends within one, is one thread's
     if (threadIdx.x == NT - 1 && end < items) {
@@ -157,14 +144,6 @@ struct RowItems {
       g.load_end(x, end, items);
       f(end, g);
     }
-  }
-  template <typename F>
-  __device__ __forceinline__ void fill(F f) const {
-    walk<true>(f);
-  }
-  template <typename F>
-  __device__ __forceinline__ void each_granule(F f) const {
-    walk<false>(f);
   }
   // Scores: -inf for items that can't be drawn.
   template <typename F>
@@ -326,6 +305,23 @@ __device__ __forceinline__ U sort_from(U v, int size, bool counts, U *buf, int &
   if constexpr (K < NT) v = sort_from<NT, 2 * K>(v, size, counts, buf, turn);
   return v;
 }
+// The sum of the threads before this one.
+template <int NT>
+__device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t *tmp) {
+  uint64_t run = v;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const uint64_t y = __shfl_up(run, o);
+    if (lane_id() >= o) run += y;
+  }
+  __syncthreads();
+  if (lane_id() == kWave - 1) tmp[threadIdx.x / kWave] = run;
+  __syncthreads();
+  run -= v;
+  for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
+  return run;
+}
+
 // Sorts one value per thread of the first `size` threads (a power of two from
 // 64) in descending order by the bitonic network; buf holds 2 NT.
 template <int NT, typename U>
@@ -508,10 +504,112 @@ __device__ Drawn select_prefix(const Items &items, Scale sc, Filters flt, float 
   return race.key ? Drawn{race.key, race.index} : Drawn{best, first};
 }
 
+// The winner, or where no score is a number the first item.
+template <int NT>
+__device__ __forceinline__ Drawn settle(Race &race, uint32_t best, uint32_t first, uint64_t *bins, uint64_t *tmp) {
+  race.block_join<NT>(bins);
+  if (race.key) return Drawn{race.key, race.index};
+  return Drawn{best, ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp))};
+}
+
+// The last item, in order of rank, above which the items at or above `lower`
+// total less than `target` (counts, or masses), as a list has it; 0 if there
+// is none.  Linear bins of log2 w (`per` to one, so that few lanes meet in one),
+// then the items of the edge's bin, sorted.  False if those are too many.
+template <bool kMassed, int NT, typename Items>
+__device__ bool find_edge(const Items &items, Scale sc, float per_unit, uint64_t lower, uint64_t target, uint64_t *buf,
+                          uint64_t *edge_list, int *listed, uint64_t *tmp, uint64_t &last) {
+  uint32_t *bins = reinterpret_cast<uint32_t *>(buf);
+  const auto bin_of = [&](uint32_t q) {
+    return min(static_cast<int>((sc.top - of_key(q)) * sc.f * per_unit), kBins - 1);  // the conversion saturates
+  };
+  const auto counts = [&](int i, uint32_t q) {
+    return q != 0 && (static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i)) >= lower;
+  };
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += NT) bins[i] = 0;
+  if (threadIdx.x == 0) *listed = 0;
+  __syncthreads();
+  items.each([&](int i, uint32_t q) {
+    if (counts(i, q)) atomicAdd(&bins[bin_of(q)], kMassed ? sc.mass(of_key(q)) : 1u);
+  });
+  __syncthreads();
+  constexpr int per = kBins / NT;
+  uint64_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < per; ++j) mine += bins[threadIdx.x * per + j];
+  uint64_t run = block_before<NT>(mine, tmp);
+  int edge = -1;
+  uint64_t edge_above = 0;
+#pragma unroll
+  for (int j = 0; j < per; ++j) {
+    const uint32_t c = bins[threadIdx.x * per + j];
+    if (c != 0 && run < target) edge = threadIdx.x * per + j, edge_above = run;
+    run += c;
+  }
+  const int bin = static_cast<int>(block_max<NT>(static_cast<uint64_t>(edge + 1), tmp)) - 1;
+  if (bin < 0) {
+    last = 0;
+    return true;
+  }
+  if (edge == bin) tmp[16] = edge_above;
+  __syncthreads();
+  const uint64_t above = tmp[16];
+  items.each([&](int i, uint32_t q) {
+    if (counts(i, q) && bin_of(q) == bin) {
+      const int at = atomicAdd(listed, 1);
+      if (at < NT) edge_list[at] = static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i);
+    }
+  });
+  __syncthreads();
+  const int n = *listed;
+  if (n > NT) return false;
+  int size = kWave;
+  while (size < n) size <<= 1;
+  const uint64_t c = block_sort<NT, uint64_t>(static_cast<int>(threadIdx.x) < n ? edge_list[threadIdx.x] : 0ull, size, buf);
+  const bool real = static_cast<int>(threadIdx.x) < n;
+  run = above + block_before<NT>(real ? (kMassed ? sc.mass(of_key(static_cast<uint32_t>(c >> 32))) : 1u) : 0u, tmp);
+  // the lowest in rank of those below the target; complemented, so that it is the largest
+  last = ~block_max<NT>(real && run < target ? ~c : 0ull, tmp);
+  return true;
+}
+
+// The kept prefix and its race, over a list or a row, with find_edge.  all,
+// as for select_prefix.  False if an edge lies among too many equal items.
+template <int NT, typename Items>
+__device__ bool select_edges(const Items &items, Scale sc, float per_unit, Filters flt, float divisor, const float *noise,
+                             bool all, uint64_t *buf, uint64_t *edge_list, int *listed, uint64_t *tmp, Drawn &drawn) {
+  uint64_t last = 0;
+  if (flt.k > 0 && !find_edge<false, NT>(items, sc, per_unit, 0, static_cast<uint64_t>(flt.k), buf, edge_list, listed, tmp, last))
+    return false;
+  if (flt.p < 1.f) {
+    uint64_t total = 0;
+    items.each([&](int i, uint32_t q) {
+      if (q != 0 && (static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i)) >= last) total += sc.mass(of_key(q));
+    });
+    total = block_sum<NT>(total, tmp);
+    if (flt.k == 0 && !all) total = static_cast<uint64_t>(kUnits);
+    uint64_t edge;
+    if (!find_edge<true, NT>(items, sc, per_unit, last, share_of(total, flt.p), buf, edge_list, listed, tmp, edge)) return false;
+    if (edge != 0) last = edge;
+  }
+  const uint32_t best = key_of(sc.top);
+  uint32_t first = 0xffffffffu;
+  Race race;
+  items.each([&](int i, uint32_t q) {
+    if (q == best) first = min(first, static_cast<uint32_t>(i));
+    if (q == 0 || (static_cast<uint64_t>(q) << 32 | ~static_cast<uint32_t>(i)) < last) return;
+    const float y = of_key(q);
+    if (sc.weight(y) >= flt.min) race.enter(noise ? y / divisor - logf(noise[i]) : y, q, static_cast<uint32_t>(i));
+  });
+  drawn = settle<NT>(race, best, first, buf, tmp);
+  return true;
+}
+
 // The race over the items of a row that `kept(y)` says stay, and that have
 // min-p's weight; `seen(i, y)` is called for every item.  first: the lowest index of the best score.
-template <typename T, int NT, int H, typename Kept, typename Seen>
-__device__ void race_row(const RowItems<T, NT, H> &row, Scale sc, float least, float divisor, const float *noise, Race &race,
+template <typename T, int NT, typename Kept, typename Seen>
+__device__ void race_row(const RowItems<T, NT> &row, Scale sc, float least, float divisor, const float *noise, Race &race,
                          uint32_t &first, Kept stays, Seen seen) {
   using G = Granule<T>;
   row.each_granule([&](int at, const G &g) {
@@ -532,20 +630,12 @@ __device__ void race_row(const RowItems<T, NT, H> &row, Scale sc, float least, f
   });
 }
 
-// The winner, or where no score is a number the first item.
-template <int NT>
-__device__ __forceinline__ Drawn settle(Race &race, uint32_t best, uint32_t first, uint64_t *bins, uint64_t *tmp) {
-  race.block_join<NT>(bins);
-  if (race.key) return Drawn{race.key, race.index};
-  return Drawn{best, ~static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(~first), tmp))};
-}
-
 // Top-p alone, for rows whose prefix is long: masses by linear bins of
 // log2 w (1/64 wide, so that few lanes meet in one; a histogram of float
 // bits has its items in a few dozen); then the bins above the edge's race, while the items of the edge's
 // bin go to a list, whose kept ones, once sorted, race too.  False if those are too many (equal scores).
-template <typename T, int NT, int H>
-__device__ bool select_share(const RowItems<T, NT, H> &items, Scale sc, Filters flt, float divisor, const float *noise,
+template <typename T, int NT>
+__device__ bool select_share(const RowItems<T, NT> &items, Scale sc, Filters flt, float divisor, const float *noise,
                              uint64_t *buf, uint64_t *list, int *listed, uint64_t *tmp, Drawn &drawn) {
   uint32_t *bins = reinterpret_cast<uint32_t *>(buf);
   const auto bin_of = [&](float y) {
@@ -570,17 +660,7 @@ __device__ bool select_share(const RowItems<T, NT, H> &items, Scale sc, Filters 
   uint64_t mine = 0;
 #pragma unroll
   for (int j = 0; j < per; ++j) mine += bins[threadIdx.x * per + j];
-  uint64_t run = mine;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint64_t y = __shfl_up(run, o);
-    if (lane_id() >= o) run += y;
-  }
-  __syncthreads();
-  if (lane_id() == kWave - 1) tmp[threadIdx.x / kWave] = run;
-  __syncthreads();
-  run -= mine;
-  for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
+  uint64_t run = block_before<NT>(mine, tmp);
   int edge = -1;  // the last bin with any mass whose items have less than the goal above them
   uint64_t edge_above = 0;
 #pragma unroll
@@ -611,17 +691,7 @@ __device__ bool select_share(const RowItems<T, NT, H> &items, Scale sc, Filters 
   const uint64_t c = block_sort<NT, uint64_t>(static_cast<int>(threadIdx.x) < n ? list[threadIdx.x] : 0ull, size, buf);
   const bool real = static_cast<int>(threadIdx.x) < n;
   mine = real ? sc.mass(of_key(static_cast<uint32_t>(c >> 32))) : 0;
-  run = mine;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint64_t y = __shfl_up(run, o);
-    if (lane_id() >= o) run += y;
-  }
-  __syncthreads();
-  if (lane_id() == kWave - 1) tmp[threadIdx.x / kWave] = run;
-  __syncthreads();
-  run += above - mine;
-  for (int w = 0; w < static_cast<int>(threadIdx.x) / kWave; ++w) run += tmp[w];
+  run = above + block_before<NT>(mine, tmp);
   if (real && run < goal) {
     const float y = of_key(static_cast<uint32_t>(c >> 32));
     const uint32_t i = ~static_cast<uint32_t>(c);
@@ -632,17 +702,15 @@ __device__ bool select_share(const RowItems<T, NT, H> &items, Scale sc, Filters 
 }
 
 // kOne: an item per thread covers the row, and the sort takes it as it is.
-// Longer rows are read from memory once as far as LDS holds them (5 granules
-// a thread, 40,960 16-bit or 20,480 fp32 scores), and again by each later pass
-// beyond that: a second pass over 131,072 bf16 scores per CU costs 15 us from
-// memory.  Held in registers, granules spilled.
+// Longer rows are read again by each pass, which the caches serve (held in
+// registers, granules spilled; held in LDS, a third to all of a row, every
+// measured case took as long or longer).
 template <typename T, int NT, bool kOne>
 __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   using G = Granule<T>;
-  constexpr int H = kOne ? 0 : 5;
   __shared__ uint64_t bins[kBins / 2 > 2 * NT ? kBins / 2 : 2 * NT];  // a histogram, or a sort's buffers
   __shared__ uint64_t list[kOne ? 1 : kList];
-  __shared__ u4 row_held[kOne ? 1 : H * NT];
+  __shared__ uint64_t edge_list[kOne ? 1 : NT];
   __shared__ uint64_t tmp[17];
   __shared__ int listed;
   constexpr int kCap = sizeof(list) / 8;
@@ -676,7 +744,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
 #pragma unroll
     for (int j = 0; j < G::N; ++j) sum += __builtin_amdgcn_exp2f((y[j] - ref) * f);
   };
-  const RowItems<T, NT, H> row{x, items, row_held};
+  const RowItems<T, NT> row{x, items};
   Race race;
   uint64_t own = 0;  // kOne: this thread's item, as a list has it
   if constexpr (kOne) {
@@ -706,7 +774,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
       }
     }
   } else {
-    row.fill([&](int, const G &g) { take(g); });
+    row.each_granule([&](int, const G &g) { take(g); });
   }
   const uint32_t best = static_cast<uint32_t>(block_max<NT>(static_cast<uint64_t>(item_key(mine)), tmp));
   if (best == 0) {
@@ -856,7 +924,11 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
         li.each([&](int, uint32_t q) { all += sc.weight(of_key(q)); });
         all = block_sum<NT>(all, tmp);
         whole = flt.k > 0 || bound == 1 || all >= flt.p * sum || (min_bound > 1 && bound == min_bound);
-        if (whole) drawn = select_prefix<NT>(li, sc, flt, divisor, greedy ? nullptr : noise, bound == 1, bins, tmp);
+        // bins over what the list spans
+        const float per_unit = fminf((kBins - 1) / fmaxf((sc.top - of_key(bound)) * sc.f, 1e-3f), 1e6f);
+        if (whole && !select_edges<NT>(li, sc, bound == 1 ? 64.f : per_unit, flt, divisor, greedy ? nullptr : noise, bound == 1,
+                                       bins, edge_list, &listed, tmp, drawn))
+          drawn = select_prefix<NT>(li, sc, flt, divisor, greedy ? nullptr : noise, bound == 1, bins, tmp);
       }
     }
     if constexpr (!kOne)
@@ -865,7 +937,9 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
           uint32_t first = 0xffffffffu;
           race_row(row, sc, flt.min, divisor, noise, race, first, [](float y) { return y > -__builtin_inff(); }, [](int, float) {});
           drawn = settle<NT>(race, best, first, bins, tmp);
-        } else if (flt.k > 0 || !select_share(row, sc, flt, divisor, noise, bins, list, &listed, tmp, drawn))
+        } else if (flt.k > 0 ? !select_edges<NT>(row, sc, 64.f, flt, divisor, greedy ? nullptr : noise, true, bins, edge_list,
+                                                 &listed, tmp, drawn)
+                             : !select_share(row, sc, flt, divisor, noise, bins, list, &listed, tmp, drawn))
           drawn = select_prefix<NT>(row, sc, flt, divisor, greedy ? nullptr : noise, true, bins, tmp);
       }
   }
@@ -875,14 +949,21 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   }
 }
 
-// Threads by the row's length: one item per thread where the row is that short.
+// Threads by the row's length: one item per thread where the row is that
+// short; 512 up to 8,192 items (64 rows of 8,192 fp16: top-k 50 12 us, 16 with 1,024; top-p
+// 0.95 27 and 35), 1,024 beyond (128 rows of 16,384 fp32: top-k 900 29 us, 42 with 512; the
+// others within 12%).
 template <typename T>
 void launch(const SampleArgs &a, int64_t rows, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(rows);
   if (a.items <= 256)
     sample_kernel<T, 256, true><<<grid, 256, 0, stream>>>(a);
+  else if (a.items <= 512)
+    sample_kernel<T, 512, true><<<grid, 512, 0, stream>>>(a);
   else if (a.items <= 1024)
     sample_kernel<T, 1024, true><<<grid, 1024, 0, stream>>>(a);
+  else if (a.items <= 8192)
+    sample_kernel<T, 512, false><<<grid, 512, 0, stream>>>(a);
   else
     sample_kernel<T, 1024, false><<<grid, 1024, 0, stream>>>(a);
 }
