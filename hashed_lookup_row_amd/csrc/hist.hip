@@ -607,7 +607,8 @@ extern "C" hlr_status hist_append(int8_t *k_codes, int8_t *v_codes, float *k_sca
                                   int64_t v_head_stride, const int64_t *slots, int64_t tokens, hipStream_t stream) {
   const hlr_status st = check_cache(k_codes, v_codes, k_scale, v_scale, num_blocks, heads, block, dim);
   if (st != HLR_OK) return st;
-  if (tokens < 0 || tokens > kMaxN || type < 0 || type > 2) return HLR_INVALID_ARG;
+  // (a launch has at most 2^31 - 1 blocks)
+  if (tokens < 0 || tokens > kMaxN || tokens / kSpan >= kMaxN / (2 * heads) || type < 0 || type > 2) return HLR_INVALID_ARG;
   if (tokens == 0) return HLR_OK;
   if (!k || !v || !slots) return HLR_INVALID_ARG;
   const int64_t unit = type == HLR_FP32 ? 4 : 8;  // elements of 16 bytes
@@ -632,7 +633,8 @@ extern "C" hlr_status hist_read(const int8_t *k_codes, const int8_t *v_codes, co
                                 hipStream_t stream) {
   const hlr_status st = check_cache(k_codes, v_codes, k_scale, v_scale, num_blocks, heads, block, dim);
   if (st != HLR_OK) return st;
-  if (tokens < 0 || tokens > kMaxN || type < 0 || type > 2) return HLR_INVALID_ARG;
+  // (a launch has at most 2^31 - 1 blocks)
+  if (tokens < 0 || tokens > kMaxN || tokens / kSpan >= kMaxN / (2 * heads) || type < 0 || type > 2) return HLR_INVALID_ARG;
   if (tokens == 0) return HLR_OK;
   if (!slots || !out_k || !out_v) return HLR_INVALID_ARG;
   if (!aligned(slots, 8) || !aligned(out_k, 16) || !aligned(out_v, 16)) return HLR_MISALIGNED;

@@ -754,11 +754,14 @@ Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t dim, int64_
   p.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t blocks = requests * kv_heads * p.row_tiles;
   const int64_t most = (max_len + 255) / 256;
-  // With keys shared by a block's waves: enough blocks that ragged lengths even out, but none for fewer than 256
-  // tokens.  With rows of their own: only where the rows leave most of the GPU idle.
-  const int64_t want = p.keys ? 4096 : 512;
+  // With keys shared by a block's waves: two blocks per CU, or four of the smaller dims (more splits cost a join
+  // and a part each: 64 requests x 2,048, 8 heads of 128 take 37 us in one split, 43 in two, 50 in eight; 64 x 8,192, 4
+  // heads of 64 take 45, 36 and 41 in two, four and sixteen), none for fewer than 256 tokens, and one launch
+  // up to 1,024 (the GPU takes 1 us longer, the host 3 us less).  With rows of their own: only where the rows
+  // leave most of the GPU idle.
+  const int64_t want = p.keys && dim <= 64 ? 1024 : 512;
   int64_t s = blocks > 0 ? (want + blocks - 1) / blocks : 1;
-  if (!p.keys && blocks > 256) s = 1;
+  if (p.keys ? max_len <= 1024 : blocks > 256) s = 1;
   if (s > most) s = most;
   if (s < 1) s = 1;
   int64_t chunk = (max_len + s - 1) / s;
@@ -798,8 +801,8 @@ hlr_status launch_dim(const Args &a, const Plan &p, int64_t dim, int64_t request
 
 bool sizes_ok(int64_t tokens, int64_t requests, int64_t q_heads, int64_t kv_heads, int64_t dim, int64_t max_q,
               int64_t max_len) {
-  return tokens >= 0 && tokens <= kMaxN && requests >= 0 && requests <= HLR_HIST_MAX_REQUESTS && kv_heads > 0 &&
-         kv_heads <= 65535 && q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads <= 65535 && max_q >= 0 &&
+  return tokens >= 0 && requests >= 0 && requests <= HLR_HIST_MAX_REQUESTS && kv_heads > 0 && kv_heads <= 65535 &&
+         q_heads >= kv_heads && q_heads % kv_heads == 0 && q_heads <= 65535 && tokens <= kMaxN / q_heads && max_q >= 0 &&
          max_q <= kMaxN / q_heads && max_len >= 0 && max_len <= kMaxN - 65536 &&
          (dim == 32 || dim == 64 || dim == 128 || dim == 256);
 }
