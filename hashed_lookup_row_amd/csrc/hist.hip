@@ -23,7 +23,8 @@ using namespace hlr;
 // and then maps its own tile of tokens by a binary search; a scan is a few
 // thousand integer additions from L2, less than a second launch costs.  A new
 // block begins with a new token, so the thread of that token writes the
-// table entry.
+// table entry.  Latency bound: 3.8 us for 64 requests, 13 us for 4,096 with a
+// map of 250,000 places (lengths, scan, search and table one after another).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanTile = 2048;
 constexpr int kPlanGroups = 4096;
@@ -195,7 +196,9 @@ __device__ __forceinline__ uint64_t follows(const int64_t *slots, int64_t t0, in
 // elements of each of 16 tokens: a wave then reads whole rows, and a thread's
 // 16 codes of one element are one store.  A thread holds its first units between
 // the maximum and the codes; the rest of a large block (over 128 elements x 64
-// tokens) is read again, from the caches.
+// tokens) is read again, from the caches.  73,700 tokens x 8 heads x 128
+// bf16: 130 us, 3.5 TB/s of keys and values in and codes out, bound by loads in
+// flight (115 registers, four waves per SIMD); one token for each of 256 requests: 9 us.
 // The low byte of the result is the code of x (clamped, rounded to nearest
 // even by adding 1.5 * 2^23, whose steps are whole); NaN gives 0.
 __device__ __forceinline__ uint32_t code(float x, float inv) {
@@ -438,7 +441,8 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
 // ------------------------------------------------------------------ read
 // Keys: 16 codes of a token per thread.  Values: a wave takes a run of tokens
 // in one chunk of 16 slots, two elements per lane, so the chunk is read once
-// with 16-byte loads and whole rows are written.
+// with 16-byte loads and whole rows are written.  73,700 tokens x 8 heads x
+// 128 to bf16: 90 to 110 us, 4.1 to 5 TB/s.
 struct ReadArgs {
   const int8_t *codes[2];
   const float *scale[2];

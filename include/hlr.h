@@ -662,14 +662,14 @@ hlr_status hist_attention(const void *q, int32_t type, int64_t tokens, int64_t q
  *  Per row (arrays of `rows`, each nullable): temperature (default 1; not above 0:
  *  the best item), top_k (int32; not above 0: no limit), top_p (default: no
  *  limit), min_p (default 0).
- *  z = fl(x / temperature); items rank by z descending, then by index.  Kept
- *  are the first top_k; of those, the items before which less than top_p
- *  of their mass lies (mass: exp(z - max z)); of those, the ones with
- *  exp(z - max z) >= min_p; and always the first.  Drawn is the kept item with
- *  the largest z - log(noise), equal ones by rank.
+ *  Items rank by score descending, then by index.  The mass of an item is
+ *  exp((x - max x) / temperature).  Kept are the first top_k; of those, the items
+ *  before which less than top_p of their mass lies; of those, the ones of
+ *  mass min_p or more; and always the first.  Drawn is the kept item with the
+ *  largest z - log(noise), z = fl(x / temperature), equal ones by rank.
  *  out_index[rows] int64; -1 if no item can be drawn.  out_logprob[rows]: the
- *  drawn item's z - log(sum of exp z) over all items before the filters (for
- *  temperature 0 that of temperature 1); -inf with index -1.
+ *  logarithm of the drawn item's share of the mass of all items, before the
+ *  filters (for temperature 0 that of temperature 1); -inf with index -1.
  *  items at most HLR_SAMPLE_MAX_ITEMS.
  * --------------------------------------------------------------------- */
 #define HLR_SAMPLE_MAX_ITEMS (1 << 27)
