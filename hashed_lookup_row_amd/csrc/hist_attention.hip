@@ -102,11 +102,10 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // successive rows; the units of a row are permuted (xor) so that any eight of
 // those lie in different banks.
 template <int D>
-struct RowTile {
+struct RowTile {  // D = 64, 128, 256
   static constexpr int kUnits = D / 8, kKeys = 64 * kUnits, kValues = D * 8;  // units of a key row, of both tiles
   static __device__ __forceinline__ int key_at(int t, int m, int unit) {
-    const int by = kUnits >= 8 ? m & (kUnits - 1) : m >> 1 & (kUnits - 1);
-    return (t * 16 + m) * kUnits + (unit ^ by);
+    return (t * 16 + m) * kUnits + (unit ^ (m & (kUnits - 1)));
   }
   static __device__ __forceinline__ int value_at(int d, int unit) { return d * 8 + (unit ^ (d & 7)); }
 };
@@ -212,7 +211,7 @@ struct Wave {
       for (int x = 0; x < NQ; ++x) s[x][t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        const int unit = D >= 64 ? (c / 2) * 8 + 2 * g + c % 2 : g;
+        const int unit = (c / 2) * 8 + 2 * g + c % 2;
         const h8 kf = __builtin_bit_cast(h8, kt[RowTile<D>::key_at(t, n, unit)]);
 #pragma unroll
         for (int x = 0; x < NQ; ++x)

@@ -98,19 +98,12 @@ struct Granule {
     __builtin_memcpy(&raw, none, 16);
     if (first <= items - N) __builtin_memcpy(&raw, x + first, 16);
   }
-  // The granule that the row ends in: its last 16 bytes moved down, -inf past them.
+  // The granule that a row of at least one granule ends in: its last 16 bytes moved down, -inf past them.
   __device__ __forceinline__ void load_end(const T *x, int first, int items) {
     uint64_t w[2] = {kInf, kInf};
     if (first < items) {
       const int bits = (first + N - items) * static_cast<int>(8 * sizeof(T));
-      if (items >= N) {
-        __builtin_memcpy(w, x + items - N, 16);
-      } else {
-        T t[N];
-#pragma unroll
-        for (int j = 0; j < N; ++j) t[j] = j < N - items ? static_cast<T>(0.f) : x[j - (N - items)];
-        __builtin_memcpy(w, t, 16);
-      }
+      __builtin_memcpy(w, x + items - N, 16);
       if (bits < 64) {
         w[0] = w[0] >> bits | w[1] << (64 - bits);
         w[1] = w[1] >> bits | kInf << (64 - bits);
@@ -198,7 +191,6 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t *tmp) {
     const uint64_t y = __shfl_xor(v, o);
     v = y > v ? y : v;
   }
-  if (NT == kWave) return v;
   __syncthreads();
   if (lane_id() == 0) tmp[threadIdx.x / kWave] = v;
   __syncthreads();
@@ -212,7 +204,6 @@ template <int NT>
 __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *tmp) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if (NT == kWave) return v;
   __syncthreads();
   if (lane_id() == 0) tmp[threadIdx.x / kWave] = v;
   __syncthreads();
@@ -226,7 +217,6 @@ template <int NT>
 __device__ __forceinline__ float block_sum(float v, uint64_t *tmp) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  if (NT == kWave) return v;
   float *t = reinterpret_cast<float *>(tmp);
   __syncthreads();
   if (lane_id() == 0) t[threadIdx.x / kWave] = v;
@@ -424,7 +414,6 @@ struct Race {
       y.index = static_cast<uint32_t>(__shfl_xor(static_cast<int>(index), o));
       meet(y);
     }
-    if (NT == kWave) return;
     __syncthreads();
     if (lane_id() == 0) {
       buf[threadIdx.x / kWave] = static_cast<uint64_t>(key) << 32 | index;
