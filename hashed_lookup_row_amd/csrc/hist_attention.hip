@@ -751,9 +751,13 @@ constexpr int row_tiles_of(int dim) { return dim == 256 ? 1 : 2; }
 Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t dim, int64_t max_q, int64_t max_len) {
   Plan p{};
   const int64_t rows = max_q * group;
-  p.keys = rows <= 16;
-  p.nq = p.keys ? 1 : row_tiles_of(static_cast<int>(dim));
-  const int64_t per = p.keys ? 16 : 16 * p.nq * kWaves;
+  // Keys shared by a block's waves: for one tile of rows; and for up to 64 rows (in tiles of 32) of long histories,
+  // where waves with rows of their own would mostly have none (64 requests x up to 4,096, 4 heads of 128: 32 rows 70 us
+  // against 94, 64 rows 97 against 109; 2 heads of 64, 24 rows: 33 against 61).  Not for short ones (256 requests x
+  // 300: 49 against 34, the join weighs more than the tiles) nor for D = 256 (56 against 55).
+  p.keys = rows <= 16 || (rows <= 64 && dim <= 128 && max_len >= 1024);
+  p.nq = !p.keys ? row_tiles_of(static_cast<int>(dim)) : rows <= 16 ? 1 : 2;
+  const int64_t per = p.keys ? 16 * p.nq : 16 * p.nq * kWaves;
   p.row_tiles = static_cast<int>((rows + per - 1) / per);
   const int64_t blocks = requests * kv_heads * p.row_tiles;
   const int64_t most = (max_len + 255) / 256;
@@ -778,9 +782,11 @@ Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t dim, int64_
 template <typename T, int D>
 hlr_status launch(const Args &a, const Plan &p, int64_t requests, hipStream_t stream) {
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.splits) * p.row_tiles * a.kv_heads * requests);
-  if (p.keys)
+  if (p.keys && p.nq == 1) {
     attention_kernel<T, D, 1, true><<<grid, kWaves * kWave, 0, stream>>>(a);
-  else if constexpr (D == 32)
+  } else if (p.keys) {
+    if constexpr (D <= 128) attention_kernel<T, D, 2, true><<<grid, kWaves * kWave, 0, stream>>>(a);
+  } else if constexpr (D == 32)
     attention_kernel<T, D, row_tiles_of(D), false><<<grid, kWaves * kWave, 0, stream>>>(a);
   else
     rows_kernel<T, D, row_tiles_of(D)><<<grid, kWaves * kWave, 0, stream>>>(a);

@@ -372,6 +372,18 @@ def test_row_counts_around_the_tiles(dev, group, new):
     check(cache, queries(dev, 3 * new, 2 * group, 64, "bf16", 6), [0, new, 2 * new, 3 * new])
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("D,kv,group,new,window", [(32, 1, 17, 1, 0), (64, 2, 8, 3, 0), (128, 1, 16, 2, 700), (128, 2, 11, 5, 0),
+                                                   (64, 1, 16, 4, 0), (256, 1, 9, 3, 0)])
+def test_few_queries_of_long_histories(dev, dtype, D, kv, group, new, window):
+    """17 to 64 rows per key head: the waves of a block share keys, in one or two tiles of 32 rows."""
+    held = [1500, new, 300, 2049, 1]
+    cache = Cache(dev, held, kv, 32, D, 31)
+    cu = [0, new, 2 * new, 2 * new, 3 * new, 3 * new + 1]
+    check(cache, queries(dev, cu[-1], kv * group, D, dtype, 32), cu, window=window)
+    check(cache, queries(dev, cu[-1], kv * group, D, dtype, 33), cu, causal=False)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_rows_that_see_nothing(dev, causal):
     """No history, queries before its first event, no blocks at all, lost blocks."""
