@@ -56,6 +56,12 @@ class HistoryCache:
     def _on_stream(self):
         return torch.cuda.stream(self.stream if self.stream is not None else torch.cuda.current_stream(self.device))
 
+    def _offsets(self, counts):
+        at = [0]
+        for c in counts:
+            at.append(at[-1] + c)
+        return torch.tensor(at, dtype=torch.int32).to(self.device, non_blocking=True)
+
     def append(self, k, v, new):
         """Adds new[u] events to each user's history: k, v [sum(new), heads, dim], users in order.  Returns the
         slots (int64 [sum(new)])."""
@@ -84,7 +90,8 @@ class HistoryCache:
 
     def attend(self, q, counts=None, window=0, scale=None, return_lse=False):
         """Attention of q [tokens, q_heads, dim] over the histories.  counts None: q are the newest events, one for
-        each event of the last append, each seeing what came before it (the last `window` events if given).
+        each event of the last append, each seeing what came before it (the last `window` events if given); users
+        released since then have none.
         counts: queries per user that see the whole history and not each other (candidates)."""
         causal = counts is None
         n = self._newest if causal else [int(c) for c in counts]
@@ -92,13 +99,7 @@ class HistoryCache:
             raise HLRError("q must hold one entry per query")
         max_q, max_len = max(n, default=0), max(self.held, default=0)
         with self._on_stream():
-            if causal:
-                cu = self.cu
-            else:
-                at = [0]
-                for c in n:
-                    at.append(at[-1] + c)
-                cu = torch.tensor(at, dtype=torch.int32).to(self.device, non_blocking=True)
+            cu = self.cu if causal else self._offsets(n)
             need = hist_attention_workspace_size(q.shape[0], self.users, q.shape[1], self.heads, self.dim, max_q, max_len)
             if need and (self._ws is None or self._ws.numel() < need + 256):
                 self._ws = new_workspace(self.device, int(need * 1.25))
@@ -116,9 +117,11 @@ class HistoryCache:
     def release(self, user):
         """Forgets the user's history; its blocks can be handed out again."""
         self._free += self.blocks[user]
-        self.blocks[user], self.held[user], self._newest[user] = [], 0, 0
+        gone, self.blocks[user], self.held[user], self._newest[user] = self._newest[user], [], 0, 0
         with self._on_stream():
             self.table[user].fill_(-1)
             self.lengths[user].zero_()
+            if gone:  # the newest events are those of the users left
+                self.cu = self._offsets(self._newest)
             self._free_dev = torch.tensor(self._free, dtype=torch.int32).to(self.device, non_blocking=True)
         self._taken = 0

@@ -108,3 +108,32 @@ def test_serving_example(dev, capsys):
     assert "us a step" in capsys.readouterr().out
     assert last.shape == (7,) and bool((last > 0).all())
     assert bool((logprob <= 0).all()) and bool(torch.isfinite(logprob).all())
+
+
+@pytest.mark.parametrize("gone", [[0], [1], [4], [3, 0], [0, 1, 2, 3, 4]])
+def test_released_users_have_no_queries_left(dev, gone):
+    """The newest events, once some of their users are released: the others' queries, users in order."""
+    users, heads, D, new = 5, 2, 64, [2, 3, 0, 1, 70]
+    cache = HistoryCache(users, 40, heads, D, 150, dev, block=16)
+    g = torch.Generator(device=dev)
+    g.manual_seed(7)
+    kv = torch.randn((2, 50, heads, D), generator=g, device=dev)
+    cache.append(kv[0], kv[1], [10, 20, 5, 15, 0])
+    kv = torch.randn((2, sum(new), heads, D), generator=g, device=dev)
+    cache.append(kv[0], kv[1], new)
+    for u in gone:
+        cache.release(u)
+    left = [0 if u in gone else n for u, n in enumerate(new)]
+    q = torch.randn((sum(left), 4, D), generator=g, device=dev)
+    out = cache.attend(q)
+    at = 0
+    for u, m in enumerate(left):
+        if m:
+            k, v = cache.read(u)
+            hidden = torch.arange(len(k))[None] > (len(k) - m + torch.arange(m))[:, None]
+            want = attention64(q[at:at + m], k, v, hidden)
+            # the bound of the growing histories above
+            assert float((out[at:at + m].double().cpu() - want).abs().max()) < 72 * 2.0 ** -23 * 8
+        at += m
+    with pytest.raises(hlr.HLRError):
+        cache.attend(torch.zeros((sum(new), 4, D), device=dev))  # rows of users that are gone
