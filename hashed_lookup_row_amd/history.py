@@ -6,6 +6,8 @@ The host decides how many events each user gains, so it knows every length and w
 enqueued, and nothing synchronises.  The table itself, the slots and the lengths are made on the GPU."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (HLRError, hist_append, hist_attention, hist_attention_workspace_size, hist_plan, hist_read,
@@ -14,8 +16,9 @@ from . import (HLRError, hist_append, hist_attention, hist_attention_workspace_s
 
 class HistoryCache:
     """users: rows of the block table; num_blocks blocks of `block` events for all of them; max_len: the longest
-    history.  stream: the torch stream the cache's kernels run on (None: the current stream at each call); calls for
-    one cache must be ordered on one stream."""
+    history.  stream: the torch stream the cache's kernels run on (None: the current stream at each call, and calls for
+    one cache must then be ordered on one stream).  A given stream waits at each call for what the current stream has
+    enqueued, and the current stream for the call, so inputs and results are used as if it were the cache's stream."""
 
     def __init__(self, users, num_blocks, heads, dim, max_len, device, block=64, stream=None):
         if block not in (16, 32, 64, 128, 256):
@@ -53,8 +56,25 @@ class HistoryCache:
     def free_blocks(self) -> int:
         return len(self._free)
 
-    def _on_stream(self):
-        return torch.cuda.stream(self.stream if self.stream is not None else torch.cuda.current_stream(self.device))
+    @contextlib.contextmanager
+    def _on_stream(self, *inputs):
+        """The cache's stream between two waits: inputs come from the current stream, which the results appended to
+        the list that this yields go to."""
+        here, results = torch.cuda.current_stream(self.device), []
+        apart = self.stream is not None and self.stream != here
+        if apart:
+            self.stream.wait_stream(here)
+        try:
+            with torch.cuda.stream(self.stream if apart else here):
+                yield results
+        finally:
+            if apart:
+                here.wait_stream(self.stream)
+        if apart:
+            for t in inputs:  # the allocator keeps them for the other stream too
+                t.record_stream(self.stream)
+            for t in results:
+                t.record_stream(here)
 
     def _offsets(self, counts):
         at = [0]
@@ -76,10 +96,11 @@ class HistoryCache:
         need = [-(-a // B) - len(b) for a, b in zip(after, self.blocks)]
         if sum(need) > len(self._free):
             raise HLRError(f"not enough free blocks: {sum(need)} needed, {len(self._free)} left")
-        with self._on_stream():
+        with self._on_stream(k, v) as results:
             fresh = torch.tensor(new, dtype=torch.int32).to(self.device, non_blocking=True)
             slots, cu, lengths, _ = hist_plan(self.lengths, fresh, self.table, self._free_dev[self._taken:], B, total)
             hist_append(*self.tensors(), k, v, slots)  # refused: the next append plans the same blocks again
+            results.append(slots)
         self.cu, self.lengths = cu, lengths
         for u, n in enumerate(need):
             self.blocks[u] += self._free[:n]
@@ -98,21 +119,24 @@ class HistoryCache:
         if len(n) != self.users or sum(n) != q.shape[0]:
             raise HLRError("q must hold one entry per query")
         max_q, max_len = max(n, default=0), max(self.held, default=0)
-        with self._on_stream():
+        with self._on_stream(q) as results:
             cu = self.cu if causal else self._offsets(n)
             need = hist_attention_workspace_size(q.shape[0], self.users, q.shape[1], self.heads, self.dim, max_q, max_len)
             if need and (self._ws is None or self._ws.numel() < need + 256):
                 self._ws = new_workspace(self.device, int(need * 1.25))
-            return hist_attention(q, *self.tensors(), self.table, self.lengths, cu, max_q, max_len, scale=scale,
-                                  causal=causal, window=window, return_lse=return_lse, ws=self._ws)
+            out = hist_attention(q, *self.tensors(), self.table, self.lengths, cu, max_q, max_len, scale=scale,
+                                 causal=causal, window=window, return_lse=return_lse, ws=self._ws)
+            results += out if return_lse else [out]
+        return out
 
     def read(self, user, dtype=torch.float32):
         """The keys and values the user's history stands for: (k, v), each [events, heads, dim]."""
         B = self.block
         slots = [b * B + i for b in self.blocks[user] for i in range(B)][:self.held[user]]
-        with self._on_stream():
+        with self._on_stream() as results:
             at = torch.tensor(slots, dtype=torch.int64).to(self.device, non_blocking=True)
-            return hist_read(*self.tensors(), at, dtype=dtype)
+            results += hist_read(*self.tensors(), at, dtype=dtype)
+        return tuple(results)
 
     def release(self, user):
         """Forgets the user's history; its blocks can be handed out again."""

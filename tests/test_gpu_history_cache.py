@@ -137,3 +137,47 @@ def test_released_users_have_no_queries_left(dev, gone):
         at += m
     with pytest.raises(hlr.HLRError):
         cache.attend(torch.zeros((sum(new), 4, D), device=dev))  # rows of users that are gone
+
+
+@pytest.mark.parametrize("return_lse", [False, True])
+def test_a_stream_of_its_own_is_ordered_with_the_callers(dev, return_lse):
+    """Inputs that the current stream has yet to make, overwritten and dropped right after the call, and results used
+    at once, while the cache runs on another stream: the same as on one stream."""
+    users, heads, D, steps = 6, 2, 64, 4
+    g = torch.Generator(device=dev)
+    g.manual_seed(9)
+    new = [[40, 3, 0, 17, 64, 1], [1, 1, 1, 1, 1, 1], [0, 9, 33, 2, 0, 5], [2, 0, 1, 1, 30, 1]]
+    data = [torch.randn((sum(n), 3, 4, D), generator=g, device=dev) for n in new]
+    busy = torch.randn((8192, 8192), generator=g, device=dev).to(torch.bfloat16)
+
+    def run(stream):
+        cache = HistoryCache(users, 60, heads, D, 200, dev, block=16, stream=stream)
+        got = []
+        for n, x in zip(new, data):
+            qkv = torch.full_like(x, 1e4)
+            for _ in range(20):  # about 15 ms that the inputs come after
+                busy @ busy
+            qkv.copy_(x)
+            q, k, v = qkv[:, 0].clone(), qkv[:, 1, :heads].clone(), qkv[:, 2, :heads].clone()
+            got.append(cache.append(k, v, n).clone())
+            k.fill_(-1e4)
+            v.fill_(-1e4)
+            del k, v
+            for c in (None, [2, 0, 1, 0, 3, 1]):
+                part = q if c is None else q[:7] if len(q) >= 7 else q.repeat(2, 1, 1)[:7]
+                part = part.clone()
+                out = cache.attend(part, counts=c, return_lse=return_lse)
+                part.fill_(1e4)
+                got += [t.clone() for t in (out if return_lse else (out,))]
+                del part, out
+                torch.full((64, 4, D), 1e4, device=dev)  # takes freed memory
+            got += [t.clone() for t in cache.read(4)]
+        cache.release(1)
+        got.append(cache.lengths.clone())
+        return got
+
+    want, got = run(None), run(torch.cuda.Stream(dev))
+    torch.cuda.synchronize()
+    assert len(want) == len(got)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
