@@ -31,6 +31,17 @@ constexpr int kPlanGroups = 4096;
 
 __device__ __forceinline__ int sat32(int64_t x) { return x > 0x7fffffff ? 0x7fffffff : static_cast<int>(x); }
 
+__device__ __forceinline__ int length_after(int cached, int fresh) {
+  return sat32(static_cast<int64_t>(max(cached, 0)) + max(fresh, 0));
+}
+
+// The new lengths alone, in the place of cached or fresh: every block of
+// plan_kernel reads those, so they are written by a launch after it.
+__global__ void __launch_bounds__(256) lengths_kernel(const int *cached, const int *fresh, int R, int *lengths) {
+  const int r = blockIdx.x * 256 + threadIdx.x;
+  if (r < R) lengths[r] = length_after(cached[r], fresh[r]);
+}
+
 // kGroups: groups of 2^group_shift requests, whose lengths are read again
 // where a token falls into one; otherwise every request has its own entry and its length is kept in LDS.
 template <bool kGroups>
@@ -90,7 +101,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       const int64_t col = (c + bmask) >> log_b, need = ((c + n + bmask) >> log_b) - col;
       if (writes) {
         cu[r] = sat32(tok_at);
-        lengths[r] = sat32(c + n);
+        if (lengths) lengths[r] = sat32(c + n);
         // tokens that find no block: the open block's, then those of new blocks
         const int64_t open = min(n, (col << log_b) - c);
         if (open > 0 && !(c >> log_b < cols && table[r * cols + (c >> log_b)] >= 0)) lost += open;
@@ -591,17 +602,35 @@ extern "C" hlr_status hist_plan(const int32_t *cached, const int32_t *fresh, int
   if (!aligned(cached, 4) || !aligned(fresh, 4) || !aligned(block_table, 4) || !aligned(free_blocks, 4) ||
       !aligned(out_slots, 8) || !aligned(out_cu, 4) || !aligned(out_lengths, 4) || !aligned(out_counts, 8))
     return HLR_MISALIGNED;
+  // every block reads the inputs while others write: no output may lie in one, except the lengths in place
+  const bool in_place = requests > 0 && (out_lengths == cached || out_lengths == fresh);
+  const struct {
+    const void *at;
+    int64_t bytes;
+    bool out;
+  } spans[] = {{cached, 4 * requests, false},          {fresh, 4 * requests, false}, {free_blocks, 4 * num_free, false},
+               {block_table, 4 * requests * table_cols, true}, {out_slots, 8 * max_tokens, true},
+               {out_cu, 4 * (requests + 1), true},     {out_counts, 16, true},
+               {out_lengths, in_place ? 0 : 4 * requests, true}};
+  for (const auto &x : spans)
+    for (const auto &y : spans)
+      if (&x != &y && x.out && x.bytes > 0 && y.bytes > 0) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(x.at), b = reinterpret_cast<uintptr_t>(y.at);
+        if (a < b + y.bytes && b < a + x.bytes) return HLR_INVALID_ARG;
+      }
   int shift = 0;
   while ((requests + (int64_t(1) << shift) - 1) >> shift > kPlanGroups) ++shift;
-  const int grid = grid_for(max_tokens, kPlanTile);
+  const int grid = grid_for(max_tokens, kPlanTile), R = static_cast<int>(requests);
+  int *lengths = in_place ? nullptr : out_lengths;
   if (shift == 0)
-    plan_kernel<false><<<grid, kPlanThreads, 0, stream>>>(cached, fresh, static_cast<int>(requests), block_table, table_cols,
-                                                          free_blocks, num_free, log_b, shift, max_tokens, out_slots,
-                                                          out_cu, out_lengths, out_counts);
+    plan_kernel<false><<<grid, kPlanThreads, 0, stream>>>(cached, fresh, R, block_table, table_cols, free_blocks, num_free,
+                                                          log_b, shift, max_tokens, out_slots, out_cu, lengths, out_counts);
   else
-    plan_kernel<true><<<grid, kPlanThreads, 0, stream>>>(cached, fresh, static_cast<int>(requests), block_table, table_cols,
-                                                         free_blocks, num_free, log_b, shift, max_tokens, out_slots,
-                                                         out_cu, out_lengths, out_counts);
+    plan_kernel<true><<<grid, kPlanThreads, 0, stream>>>(cached, fresh, R, block_table, table_cols, free_blocks, num_free,
+                                                         log_b, shift, max_tokens, out_slots, out_cu, lengths, out_counts);
+  const hlr_status st = launch_status();
+  if (st != HLR_OK || !in_place) return st;
+  lengths_kernel<<<grid_for(requests, 256), 256, 0, stream>>>(cached, fresh, R, out_lengths);
   return launch_status();
 }
 

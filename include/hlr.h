@@ -593,7 +593,9 @@ hlr_status memory_layer_step(int64_t *identity, int64_t *stamps, float *values, 
  *  out_slots[max_tokens] slot of each new token, requests in order; -1 where
  *                       its block is missing, and past the last token.
  *  out_cu[requests+1]   first token of each request, then their number.
- *  out_lengths[requests] cached + fresh.
+ *  out_lengths[requests] cached + fresh; may be `cached` or `fresh` itself, which
+ *                       costs a second launch.  No other output may overlap an
+ *                       input or another output (HLR_INVALID_ARG).
  *  out_counts[2]        int64 {blocks taken of the list, new tokens whose
  *                       block is missing}.
  *  max_tokens must hold the batch's new tokens: later ones get no slot and

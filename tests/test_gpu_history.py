@@ -103,6 +103,27 @@ def test_plan_drops_tokens_past_the_given_number(dev):
     assert table.tolist() == [[5, 6, -1, -1], [7, -1, -1, -1]]  # request 1's second block holds dropped tokens only
 
 
+@pytest.mark.parametrize("requests,new_hi,B", [(3, 5, 16), (64, 400, 64), (4096, 60, 32), (9001, 12, 16)])
+@pytest.mark.parametrize("which", ["cached", "new"])
+def test_plan_with_the_lengths_in_place(dev, requests, new_hi, B, which):
+    """lengths written over cached or new: the same as apart, step by step."""
+    g = torch.Generator(device=dev)
+    g.manual_seed(requests)
+    free = torch.randperm(requests * 30, generator=g, device=dev).to(torch.int32)
+    tables = [torch.full((requests, 9 * new_hi // B + 2), -1, dtype=torch.int32, device=dev) for _ in range(2)]
+    cached, taken, B8 = torch.zeros(requests, dtype=torch.int32, device=dev), 0, requests * new_hi
+    for step in range(8):
+        new = torch.randint(-1, new_hi + 1, (requests,), generator=g, device=dev).to(torch.int32)
+        a = hlr.hist_plan(cached, new, tables[0], free[taken:], B, B8)
+        c, n = cached.clone(), new.clone()
+        out = tuple(torch.empty_like(t) for t in a[:2]) + (c if which == "cached" else n, torch.empty_like(a[3]))
+        b = hlr.hist_plan(c, n, tables[1], free[taken:], B, B8, out=out)
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+        assert torch.equal(*tables)
+        cached, taken = a[2], taken + int(a[3][0])
+
+
 # ---------------------------------------------------------------- append
 class Pool:
     """A cache with garbage in it, and a host copy that follows the definition in fp32."""

@@ -35,6 +35,27 @@ def test_plan(lib):
     assert plan(lib, requests=2, cached=ODD) == MISALIGNED
 
 
+def test_plan_refuses_outputs_that_overlap(lib):
+    at = [ctypes.c_void_p((1 << 20) + (i << 12)) for i in range(8)]
+    names = ("cached", "fresh", "table", "free", "slots", "cu", "lengths", "counts")
+    size = {"cached": 28, "fresh": 28, "table": 7 * 3 * 4, "free": 20, "slots": 72, "cu": 32, "lengths": 28, "counts": 16}
+
+    def call(**other):
+        a = dict(zip(names, at), **other)
+        return lib.hist_plan(a["cached"], a["fresh"], 7, a["table"], 3, a["free"], 5, 16, 9, a["slots"], a["cu"], a["lengths"],
+                             a["counts"], None)
+
+    for x in ("table", "slots", "cu", "lengths", "counts"):
+        for y in names:
+            if x == y or (x == "lengths" and y in ("cached", "fresh")):
+                continue
+            assert call(**{x: at[names.index(y)]}) == INVALID, (x, y)
+            last = at[names.index(y)].value + (size[y] - 1) // 8 * 8  # one element shared
+            assert call(**{x: ctypes.c_void_p(last)}) == INVALID, (x, y)
+    for y in ("cached", "fresh"):  # the lengths in place are right, but not moved by an element
+        assert call(lengths=ctypes.c_void_p(at[names.index(y)].value + 4)) == INVALID
+
+
 def append(lib, blocks=4, heads=2, block=16, dim=64, k=P, type_=1, kt=128, kh=64, slots=P, tokens=3, codes=P):
     return lib.hist_append(codes, P, P, P, blocks, heads, block, dim, k, P, type_, kt, kh, 128, 64, slots, tokens, None)
 
