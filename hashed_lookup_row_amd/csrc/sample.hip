@@ -722,7 +722,9 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   if (!(flt.p < 1.f)) flt.p = 1.f;
   if (greedy) flt = Filters{items > 1 ? 1 : 0, 1.f, 0.f};
   const bool open = !greedy && flt.k == 0 && flt.p == 1.f && !(flt.min > 0.f);  // every item may win
-  const float f = fminf(kLog2e / divisor, kMost);
+  // not 0, where -inf x 0 is no number: at an infinite temperature scores within 3.4e38 of the best weigh 1 (less 2^-21
+  // at the most), -inf 0
+  const float f = fminf(fmaxf(kLog2e / divisor, 1.401298464e-45f), kMost);
 
   // 1. maxima, and the sum of w against the thread's own maximum
   float mine = -__builtin_inff(), ref = -kMost, sum = 0.f;

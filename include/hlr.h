@@ -662,8 +662,8 @@ hlr_status hist_attention(const void *q, int32_t type, int64_t tokens, int64_t q
  *  are items that can't be drawn, +inf counts as the largest number.
  *  noise[rows][items] fp32, positive, distributed as Exp(1).
  *  Per row (arrays of `rows`, each nullable): temperature (default 1; not above 0:
- *  the best item), top_k (int32; not above 0: no limit), top_p (default: no
- *  limit), min_p (default 0).
+ *  the best item; +inf: items that can be drawn weigh the same), top_k (int32;
+ *  not above 0: no limit), top_p (default: no limit), min_p (default 0).
  *  Items rank by score descending, then by index.  The mass of an item is
  *  exp((x - max x) / temperature).  Kept are the first top_k; of those, the items
  *  before which less than top_p of their mass lies; of those, the ones of

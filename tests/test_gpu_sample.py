@@ -180,6 +180,35 @@ def test_masked_and_odd_values(dev):
     assert abs(float(logprob[5]) + math.log(V)) < 1e-5
 
 
+@pytest.mark.parametrize("V", [90, 700, 3000, 20_000, 70_000])
+def test_infinite_temperature(dev, V):
+    """Every item that can be drawn weighs the same; rank still goes by score."""
+    R = 8
+    x, e = inputs(dev, R, V, "fp32", V)
+    x[:, ::3] = -math.inf
+    x[:, 1::7] = math.nan
+    x[5, :] = -math.inf
+    x[5, V // 2] = 3.0
+    xs, es = x.cpu().numpy(), e.cpu().numpy()
+    for t in (math.inf, 3e38):
+        for k, p, m in ((0, 1.0, 0.0), (7, 1.0, 0.0), (0, 0.37, 0.0), (0, 1.0, 0.5), (V // 2, 0.61, 0.2), (V // 5, 1.0, 0.0)):
+            on = lambda v, dt=torch.float32: torch.full((R,), v, dtype=dt, device=dev)  # noqa: E731
+            index, logprob = hlr.sample_scores(x, e, on(t), on(k, torch.int32), on(p), on(m))
+            for r in range(R):
+                left = np.flatnonzero(xs[r] > -np.inf)
+                by = left[np.argsort(-xs[r][left], kind="stable")]
+                n = min(k, len(by)) if k else len(by)
+                if p < 1 and n > 1:
+                    # equal weights: item i is kept while i < p n, where p n is no whole number's neighbour
+                    edge = float(np.float32(p)) * n
+                    if abs(edge - round(edge)) < 1e-3:
+                        continue
+                    n = int(edge) + 1
+                kept = by[:n]
+                assert int(index[r]) == kept[np.argmin(es[r][kept])], (t, k, p, m, r)
+                assert abs(float(logprob[r]) + math.log(len(left))) <= 2.0 ** -22 * (4 + math.log(len(left)))
+
+
 def test_no_rows_no_items(dev):
     x = torch.zeros((0, 7), device=dev)
     assert hlr.sample_scores(x, x)[0].numel() == 0
