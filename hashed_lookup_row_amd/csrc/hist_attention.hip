@@ -382,10 +382,12 @@ __device__ __forceinline__ void load_values(const Args &a, Ids id, int kvh, int 
   vs = a.vs[bh];
 }
 
-// A request's length, within what its table row and the launch cover.
-__device__ __forceinline__ int length_of(const Args &a, int r) {
-  const int64_t most = min(a.cols << a.log_b, static_cast<int64_t>(a.max_len));
-  return max(0, static_cast<int>(min(static_cast<int64_t>(a.lengths[r]), most)));
+// A request's length, within what the launch covers: where its queries stand.
+__device__ __forceinline__ int length_of(const Args &a, int r) { return max(0, min(a.lengths[r], a.max_len)); }
+
+// Its positions that the table row has a place for; later ones have no block.
+__device__ __forceinline__ int held_of(const Args &a, int length) {
+  return static_cast<int>(min(static_cast<int64_t>(length), a.cols << a.log_b));
 }
 
 // Rows' results, from a wave: to the output, or to a split's part.
@@ -447,9 +449,9 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) rows_kernel(A
   const int rows = min(fresh, a.max_q) * a.group;
   const int block_row0 = rt * kWaves * 16 * NQ, row0 = block_row0 + wave * 16 * NQ;
   if (first < 0 || fresh <= 0 || block_row0 >= rows) return;
-  const int length = length_of(a, r);
+  const int length = length_of(a, r), held = held_of(a, length);
   const int64_t split_lo = static_cast<int64_t>(split) * a.chunk;
-  if (split > 0 && split_lo >= length) return;  // the combine knows that this split is empty
+  if (split > 0 && split_lo >= held) return;  // the combine knows that this split is empty
 
   W w;
   w.load_queries(a, r, kvh, min(row0, rows), rows, first, fresh, length);
@@ -458,9 +460,9 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) rows_kernel(A
   // positions that rows [b, e) see any of
   const auto span = [&](int b, int e, int &lo, int &hi) {
     lo = 0;
-    hi = b < e ? length : 0;
+    hi = b < e ? held : 0;
     if (a.causal && b < e) {
-      hi = min(length, max(0, length - fresh + (e - 1) / a.group + 1));
+      hi = min(held, max(0, length - fresh + (e - 1) / a.group + 1));
       if (a.window > 0) lo = max(0, length - fresh + b / a.group + 1 - a.window);
     }
     if (a.part) {
@@ -566,10 +568,10 @@ __global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
   const int row0 = kKeys ? rt * 16 * NQ : (rt * kWaves + wave) * 16 * NQ;
   const int block_row0 = kKeys ? row0 : rt * kWaves * 16 * NQ;
   if (first < 0 || fresh <= 0 || block_row0 >= rows) return;
-  const int length = length_of(a, r);
+  const int length = length_of(a, r), held = held_of(a, length);
   const bool splits = a.part != nullptr;
   const int64_t split_lo = static_cast<int64_t>(split) * a.chunk;
-  if (splits && split > 0 && split_lo >= length) return;  // the combine knows that this split is empty
+  if (splits && split > 0 && split_lo >= held) return;  // the combine knows that this split is empty
 
   W w;
   w.load_queries(a, r, kvh, min(row0, rows), rows, first, fresh, length);
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
     see_hi = max(see_hi, __shfl_xor(see_hi, o));
   }
   see_lo = __builtin_amdgcn_readfirstlane(see_lo);
-  see_hi = min(__builtin_amdgcn_readfirstlane(see_hi), length);
+  see_hi = min(__builtin_amdgcn_readfirstlane(see_hi), held);
   if (splits) {
     see_lo = max(see_lo, static_cast<int>(min(split_lo, int64_t(0x7fffffff))));
     see_hi = static_cast<int>(min(static_cast<int64_t>(see_hi), split_lo + a.chunk));
@@ -691,7 +693,7 @@ __global__ void __launch_bounds__(256) combine_kernel(Args a, int requests) {
   }
   if (tok < a.cu[lo] || tok >= a.cu[lo + 1]) return;
   if (tok - a.cu[lo] >= a.max_q) return;
-  const int n = max(1, static_cast<int>((static_cast<int64_t>(length_of(a, lo)) + a.chunk - 1) / a.chunk));
+  const int n = max(1, static_cast<int>((static_cast<int64_t>(held_of(a, length_of(a, lo))) + a.chunk - 1) / a.chunk));
   const int64_t step = a.tokens * heads;
   __shared__ float wave_top[4], weight[256];
   __shared__ f4 joined[kGroups][kPer];

@@ -581,6 +581,25 @@ def test_replayed_as_a_graph(dev):
         qkv.copy_(torch.randn((R, 3, kv, D), device=dev) * (1.5 ** i))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("D,group,new", [(64, 2, 3), (64, 2, 60), (32, 2, 70), (128, 1, 130), (256, 3, 40)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 90), (False, 0)])
+def test_histories_longer_than_their_table_rows(dev, dtype, D, group, new, causal, window):
+    """Positions past the table row are positions without a block: the queries stay at the history's end."""
+    held, cu = [300, 70, 1500], [0, new, 2 * new, 3 * new]
+    cache = Cache(dev, held, 2, 16, D, 41)
+    whole = cache.table
+    q = queries(dev, 3 * new, 2 * group, D, dtype, 42)
+    for cols in (1, 6, 40):
+        cache.table = whole.clone()
+        cache.table[:, cols:] = -1
+        want, wl = check(cache, q, cu, causal=causal, window=window)
+        got, gl = hlr.hist_attention(q, *cache.tensors(), whole[:, :cols].contiguous(), cache.lengths,
+                                     torch.tensor(cu, dtype=torch.int32, device=dev), new, max(held), causal=causal,
+                                     window=window, return_lse=True)
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+
+
 # --------------------------------------------------------------- refusals
 def test_refusals(dev):
     cache = Cache(dev, [20, 20], 2, 16, 64, 27)
