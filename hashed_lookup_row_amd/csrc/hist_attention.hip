@@ -66,6 +66,10 @@ struct Args {
   int max_q, max_len;  // the caller's bounds: what a launch covers
 };
 
+// The first position that a query at position `at` (below 0: before the history's first) sees through the window;
+// no difference is taken that passes 32 bits, whatever the window.
+__device__ __forceinline__ int first_seen(const Args &a, int at) { return at >= a.window ? at + 1 - a.window : 0; }
+
 __device__ __forceinline__ h8 f16_of_codes(uint32_t lo, uint32_t hi) {
   // byte b -> f16 with bits 0x64xx = 1024 + (b ^ 0x80) = 1152 + code
   lo ^= 0x80808080u;
@@ -171,7 +175,7 @@ struct Wave {
         if (a.causal) {
           const int at = length - fresh + i;
           hi[x] = max(at + 1, 0);
-          if (a.window > 0) lo[x] = max(at + 1 - a.window, 0);
+          if (a.window > 0) lo[x] = first_seen(a, at);
         }
       }
       m[x] = m2[x] = kNone;
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) rows_kernel(A
     hi = b < e ? held : 0;
     if (a.causal && b < e) {
       hi = min(held, max(0, length - fresh + (e - 1) / a.group + 1));
-      if (a.window > 0) lo = max(0, length - fresh + b / a.group + 1 - a.window);
+      if (a.window > 0) lo = first_seen(a, length - fresh + b / a.group);
     }
     if (a.part) {
       lo = max(lo, static_cast<int>(split_lo));

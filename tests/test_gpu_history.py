@@ -600,6 +600,19 @@ def test_histories_longer_than_their_table_rows(dev, dtype, D, group, new, causa
         assert torch.equal(got, want) and torch.equal(gl, wl)
 
 
+@pytest.mark.parametrize("D,group", [(32, 1), (64, 3), (128, 2), (256, 1), (64, 1)])
+def test_the_widest_windows(dev, D, group):
+    """A window of up to 2^31 - 1 hides nothing, also from requests with more queries than events."""
+    held, new = [1, 20, 400], [20, 300, 90]
+    cache = Cache(dev, held, 1, 32, D, 43)
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = queries(dev, cu[-1], group, D, "bf16", 44)
+    want, wl = check(cache, q, cu)
+    for window in (400, 401, 2 ** 31 - 400, 2 ** 31 - 2, 2 ** 31 - 1):
+        got, gl = check(cache, q, cu, window=window)
+        assert torch.equal(got, want) and torch.equal(gl, wl), window
+
+
 # --------------------------------------------------------------- refusals
 def test_refusals(dev):
     cache = Cache(dev, [20, 20], 2, 16, 64, 27)
