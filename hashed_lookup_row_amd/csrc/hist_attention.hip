@@ -286,8 +286,9 @@ struct Wave {
         m2[x] = now2;
         rel[x] = pow2(now - now2);
       }
-      // finite even where the best scores' values are all zero (a scale of 0) and m is far above m2: p is 0 there
-      const float off = kUp - m[x], c = fminf(vs * rel[x], 3.402823466e38f);
+      // finite where p is 0: the best scores' values may all be zero (a scale of 0, m far above m2), and the scale of a
+      // block that the row sees nothing of may be anything
+      const float off = kUp - m[x], c = __builtin_amdgcn_fmed3f(vs * rel[x], -3.402823466e38f, 3.402823466e38f);
       float sum = 0.f;
 #pragma unroll
       for (int t = 0; t < 4; ++t)

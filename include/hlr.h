@@ -571,7 +571,8 @@ hlr_status memory_layer_step(int64_t *identity, int64_t *stamps, float *values, 
  *  32, 64, 128 or 256 elements (else HLR_UNSUPPORTED_DIM):
  *    k_codes int8 [num_blocks][heads][block][dim]
  *    v_codes int8 [num_blocks][heads][block/16][dim][16]
- *    k_scale, v_scale fp32 [num_blocks][heads]; a value is code * scale.
+ *    k_scale, v_scale fp32 [num_blocks][heads], not negative; a value is code *
+ *    scale.  Scales and codes that no query sees may be anything.
  *  Codes are 16-byte aligned.  A slot is block id * block + place in the
  *  block (int64; -1: none).  block_table int32 [requests][table_cols] holds
  *  each request's block ids in order of position; -1: no block.

@@ -613,6 +613,30 @@ def test_the_widest_windows(dev, D, group):
         assert torch.equal(got, want) and torch.equal(gl, wl), window
 
 
+@pytest.mark.parametrize("D,group,new", [(64, 2, 1), (32, 2, 90), (64, 1, 70), (128, 4, 20), (256, 2, 40)])
+def test_scales_of_blocks_that_nobody_sees_may_be_anything(dev, D, group, new):
+    """Blocks of a table row behind the length, or before the window, in a tile with blocks that are seen."""
+    cache = Cache(dev, [112, 160, 192], 2, 16, D, 45)
+    cache.lengths = torch.tensor([100, 98, 130], dtype=torch.int32, device=dev)
+    cu = [0, new, 2 * new, 3 * new]
+    q = queries(dev, 3 * new, 2 * group, D, "bf16", 46)
+    for window in (0, 5):
+        first_seen = [max(0, n - new - window) // 16 if window else 0 for n in (100, 98, 130)]
+        want, wl = check(cache, q, cu, window=window)
+        for bad in (math.nan, math.inf, -math.inf, -3e38):
+            dirty = Cache(dev, [112, 160, 192], 2, 16, D, 45)
+            dirty.lengths = cache.lengths
+            for r, n in enumerate((100, 98, 130)):
+                blocks = dirty.table[r].tolist()
+                for col, b in enumerate(blocks):
+                    if b >= 0 and (col * 16 >= n or col < first_seen[r]):
+                        dirty.ks[b] = dirty.vs[b] = bad
+            got, gl = hlr.hist_attention(q, *dirty.tensors(), dirty.table, dirty.lengths,
+                                         torch.tensor(cu, dtype=torch.int32, device=dev), new, 130, window=window,
+                                         return_lse=True)
+            assert torch.equal(got, want) and torch.equal(gl, wl), bad
+
+
 # --------------------------------------------------------------- refusals
 def test_refusals(dev):
     cache = Cache(dev, [20, 20], 2, 16, 64, 27)
