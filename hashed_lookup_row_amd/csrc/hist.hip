@@ -250,6 +250,7 @@ struct AppendArgs {
   const int64_t *slots;
   int64_t tokens, num_slots;
   int heads, log_b, span;
+  int64_t first;  // span of this launch's first blocks
 };
 
 // 16 elements of one token.
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(NT) append_kernel(AppendArgs a) {
   const int64_t stride = a.tok_stride[which];
   __shared__ float top[2][NT / kWave];
   int turn = 0;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x / (2 * a.heads)) * a.span;
+  const int64_t t0 = (a.first + blockIdx.x / (2 * a.heads)) * a.span;
   int64_t my_slot;
   const uint64_t goes_on = follows(a.slots, t0, a.tokens, a.num_slots, a.log_b, my_slot);
   uint64_t starts = ~goes_on & ballot(my_slot >= 0);
@@ -461,6 +462,7 @@ struct ReadArgs {
   const int64_t *slots;
   int64_t tokens, num_slots;
   int heads, log_b;
+  int64_t first;  // span of this launch's first blocks
 };
 
 template <typename T>
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
   const int which = blockIdx.x / a.heads % 2, head = blockIdx.x % a.heads, tid = threadIdx.x;
   const int lane = lane_id(), wave = tid / kWave;
   T *out = static_cast<T *>(a.out[which]) + static_cast<int64_t>(head) * D;
-  const int64_t row = static_cast<int64_t>(a.heads) * D, t0 = static_cast<int64_t>(blockIdx.x / (2 * a.heads)) * kSpan;
+  const int64_t row = static_cast<int64_t>(a.heads) * D, t0 = (a.first + blockIdx.x / (2 * a.heads)) * kSpan;
   const int here = static_cast<int>(min(static_cast<int64_t>(kSpan), a.tokens - t0));
   const int in_b = (1 << a.log_b) - 1;
   if (which == 0) {
@@ -541,22 +543,32 @@ __global__ void __launch_bounds__(256) read_kernel(ReadArgs a) {
   }
 }
 
+// Blocks of NT threads for keys and values, head by head, of each span of tokens.
+template <int NT, typename A, typename Launch>
+hlr_status launch_spans(A a, int64_t span, Launch launch) {
+  const int64_t spans = grid_for(a.tokens, static_cast<int>(span)), most = most_blocks(NT) / (2 * a.heads);
+  for (; a.first < spans; a.first += most) {
+    const int64_t here = spans - a.first < most ? spans - a.first : most;
+    launch(static_cast<unsigned>(here * 2 * a.heads), a);
+    const hlr_status st = launch_status();
+    if (st != HLR_OK) return st;
+  }
+  return HLR_OK;
+}
 template <typename T, int D>
-void launch_append(const AppendArgs &a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(grid_for(a.tokens, a.span)) * 2u * static_cast<unsigned>(a.heads));
+hlr_status launch_append(const AppendArgs &a, hipStream_t stream) {
   // few tokens: a wave per token and head, since most runs are single tokens then; else a block per span
   if (a.span == 1)
-    append_kernel<T, D, 64><<<grid, 64, 0, stream>>>(a);
-  else
-    append_kernel<T, D, 256><<<grid, 256, 0, stream>>>(a);
+    return launch_spans<64>(a, 1, [&](unsigned grid, const AppendArgs &b) { append_kernel<T, D, 64><<<grid, 64, 0, stream>>>(b); });
+  return launch_spans<256>(a, a.span,
+                           [&](unsigned grid, const AppendArgs &b) { append_kernel<T, D, 256><<<grid, 256, 0, stream>>>(b); });
 }
 template <typename T, int D>
-void launch_read(const ReadArgs &a, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(grid_for(a.tokens, kSpan)) * 2u * static_cast<unsigned>(a.heads));
-  read_kernel<T, D><<<grid, 256, 0, stream>>>(a);
+hlr_status launch_read(const ReadArgs &a, hipStream_t stream) {
+  return launch_spans<256>(a, kSpan, [&](unsigned grid, const ReadArgs &b) { read_kernel<T, D><<<grid, 256, 0, stream>>>(b); });
 }
 template <typename T>
-void launch_append_dim(const AppendArgs &a, int64_t dim, hipStream_t stream) {
+hlr_status launch_append_dim(const AppendArgs &a, int64_t dim, hipStream_t stream) {
   switch (dim) {
     case 32: return launch_append<T, 32>(a, stream);
     case 64: return launch_append<T, 64>(a, stream);
@@ -565,7 +577,7 @@ void launch_append_dim(const AppendArgs &a, int64_t dim, hipStream_t stream) {
   }
 }
 template <typename T>
-void launch_read_dim(const ReadArgs &a, int64_t dim, hipStream_t stream) {
+hlr_status launch_read_dim(const ReadArgs &a, int64_t dim, hipStream_t stream) {
   switch (dim) {
     case 32: return launch_read<T, 32>(a, stream);
     case 64: return launch_read<T, 64>(a, stream);
@@ -640,8 +652,7 @@ extern "C" hlr_status hist_append(int8_t *k_codes, int8_t *v_codes, float *k_sca
                                   int64_t v_head_stride, const int64_t *slots, int64_t tokens, hipStream_t stream) {
   const hlr_status st = check_cache(k_codes, v_codes, k_scale, v_scale, num_blocks, heads, block, dim);
   if (st != HLR_OK) return st;
-  // (a launch has at most 2^31 - 1 blocks)
-  if (tokens < 0 || tokens > kMaxN || tokens / kSpan >= kMaxN / (2 * heads) || type < 0 || type > 2) return HLR_INVALID_ARG;
+  if (tokens < 0 || tokens > kMaxN || type < 0 || type > 2) return HLR_INVALID_ARG;
   if (tokens == 0) return HLR_OK;
   if (!k || !v || !slots) return HLR_INVALID_ARG;
   const int64_t unit = type == HLR_FP32 ? 4 : 8;  // elements of 16 bytes
@@ -649,15 +660,11 @@ extern "C" hlr_status hist_append(int8_t *k_codes, int8_t *v_codes, float *k_sca
       v_token_stride % unit || v_head_stride % unit)
     return HLR_MISALIGNED;
   AppendArgs a{{k, v}, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}, {k_codes, v_codes},
-               {k_scale, v_scale}, slots, tokens, num_blocks * block, static_cast<int>(heads), log2_block(block), 1};
+               {k_scale, v_scale}, slots, tokens, num_blocks * block, static_cast<int>(heads), log2_block(block), 1, 0};
   while (a.span < kSpan && tokens * heads * 2 / a.span > 8192) a.span *= 2;
-  if (type == HLR_FP32)
-    launch_append_dim<float>(a, dim, stream);
-  else if (type == HLR_BF16)
-    launch_append_dim<bf16>(a, dim, stream);
-  else
-    launch_append_dim<_Float16>(a, dim, stream);
-  return launch_status();
+  if (type == HLR_FP32) return launch_append_dim<float>(a, dim, stream);
+  if (type == HLR_BF16) return launch_append_dim<bf16>(a, dim, stream);
+  return launch_append_dim<_Float16>(a, dim, stream);
 }
 
 extern "C" hlr_status hist_read(const int8_t *k_codes, const int8_t *v_codes, const float *k_scale,
@@ -666,18 +673,13 @@ extern "C" hlr_status hist_read(const int8_t *k_codes, const int8_t *v_codes, co
                                 hipStream_t stream) {
   const hlr_status st = check_cache(k_codes, v_codes, k_scale, v_scale, num_blocks, heads, block, dim);
   if (st != HLR_OK) return st;
-  // (a launch has at most 2^31 - 1 blocks)
-  if (tokens < 0 || tokens > kMaxN || tokens / kSpan >= kMaxN / (2 * heads) || type < 0 || type > 2) return HLR_INVALID_ARG;
+  if (tokens < 0 || tokens > kMaxN || type < 0 || type > 2) return HLR_INVALID_ARG;
   if (tokens == 0) return HLR_OK;
   if (!slots || !out_k || !out_v) return HLR_INVALID_ARG;
   if (!aligned(slots, 8) || !aligned(out_k, 16) || !aligned(out_v, 16)) return HLR_MISALIGNED;
   const ReadArgs a{{k_codes, v_codes}, {k_scale, v_scale}, {out_k, out_v}, slots, tokens, num_blocks * block,
-                   static_cast<int>(heads), log2_block(block)};
-  if (type == HLR_FP32)
-    launch_read_dim<float>(a, dim, stream);
-  else if (type == HLR_BF16)
-    launch_read_dim<bf16>(a, dim, stream);
-  else
-    launch_read_dim<_Float16>(a, dim, stream);
-  return launch_status();
+                   static_cast<int>(heads), log2_block(block), 0};
+  if (type == HLR_FP32) return launch_read_dim<float>(a, dim, stream);
+  if (type == HLR_BF16) return launch_read_dim<bf16>(a, dim, stream);
+  return launch_read_dim<_Float16>(a, dim, stream);
 }

@@ -683,10 +683,10 @@ __global__ void __launch_bounds__(kWaves *kWave) attention_kernel(Args a) {
 // pass finds the largest maximum, then each of 1024 / D groups of D / 4
 // threads adds every such group's share of the splits, four elements a thread.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) combine_kernel(Args a, int requests) {
+__global__ void __launch_bounds__(256) combine_kernel(Args a, int requests, int64_t first_row) {
   constexpr int kPer = D / 4, kGroups = 256 / kPer;
   const int heads = a.kv_heads * a.group, tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int64_t row = first_row + blockIdx.x;
   const int tok = static_cast<int>(row / heads);
   int lo = 0, hi = requests;  // the last request that begins at or before tok
   while (hi - lo > 1) {
@@ -787,8 +787,7 @@ Plan plan(int64_t requests, int64_t kv_heads, int64_t group, int64_t dim, int64_
 }
 
 template <typename T, int D>
-hlr_status launch(const Args &a, const Plan &p, int64_t requests, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.splits) * p.row_tiles * a.kv_heads * requests);
+void launch_requests(const Args &a, const Plan &p, unsigned grid, hipStream_t stream) {
   if (p.keys && p.nq == 1) {
     attention_kernel<T, D, 1, true><<<grid, kWaves * kWave, 0, stream>>>(a);
   } else if (p.keys) {
@@ -797,12 +796,31 @@ hlr_status launch(const Args &a, const Plan &p, int64_t requests, hipStream_t st
     attention_kernel<T, D, row_tiles_of(D), false><<<grid, kWaves * kWave, 0, stream>>>(a);
   else
     rows_kernel<T, D, row_tiles_of(D)><<<grid, kWaves * kWave, 0, stream>>>(a);
-  if (p.splits > 1) {
+}
+
+template <typename T, int D>
+hlr_status launch(const Args &a, const Plan &p, int64_t requests, hipStream_t stream) {
+  const int64_t each = static_cast<int64_t>(p.splits) * p.row_tiles * a.kv_heads, most = most_blocks(kWaves * kWave) / each;
+  for (int64_t r = 0; r < requests; r += most) {
+    Args b = a;
+    b.table += r * a.cols;
+    b.lengths += r;
+    b.cu += r;
+    b.requests = static_cast<uint32_t>(requests - r < most ? requests - r : most);
+    launch_requests<T, D>(b, p, static_cast<unsigned>(each * b.requests), stream);
     const hlr_status st = launch_status();
     if (st != HLR_OK) return st;
-    combine_kernel<T, D><<<grid_for(a.tokens * a.kv_heads * a.group, 1), 256, 0, stream>>>(a, static_cast<int>(requests));
   }
-  return launch_status();
+  if (p.splits > 1) {
+    const int64_t rows = a.tokens * a.kv_heads * a.group;
+    for (int64_t r = 0; r < rows; r += most_blocks(256)) {
+      const int64_t here = rows - r < most_blocks(256) ? rows - r : most_blocks(256);
+      combine_kernel<T, D><<<static_cast<unsigned>(here), 256, 0, stream>>>(a, static_cast<int>(requests), r);
+      const hlr_status st = launch_status();
+      if (st != HLR_OK) return st;
+    }
+  }
+  return HLR_OK;
 }
 
 template <typename T>
@@ -859,7 +877,7 @@ extern "C" hlr_status hist_attention(const void *q, int32_t type, int64_t tokens
       !aligned(lengths, 4) || !aligned(cu, 4) || !aligned(out_lse, 4))
     return HLR_MISALIGNED;
   const Plan p = plan(requests, kv_heads, q_heads / kv_heads, dim, max_q, max_len);
-  if (static_cast<int64_t>(p.splits) * p.row_tiles > 0x7fffffff / (kv_heads * requests)) return HLR_INVALID_ARG;
+  if (static_cast<int64_t>(p.splits) * p.row_tiles > most_blocks(kWaves * kWave) / kv_heads) return HLR_INVALID_ARG;
   Args a{};
   a.q = q;
   a.q_tok = q_token_stride;
@@ -884,7 +902,6 @@ extern "C" hlr_status hist_attention(const void *q, int32_t type, int64_t tokens
   a.scale = scale * 1.44269504088896340736f;
   a.chunk = p.chunk;
   a.row_tiles = p.row_tiles;
-  a.requests = static_cast<uint32_t>(requests);
   a.splits = static_cast<uint32_t>(p.splits);
   a.max_q = static_cast<int>(max_q);
   a.max_len = static_cast<int>(max_len);

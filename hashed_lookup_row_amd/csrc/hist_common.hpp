@@ -1,4 +1,4 @@
-// Element types of the history-cache and sampling kernels.
+// Element types and launch sizes of the history-cache and sampling kernels.
 #pragma once
 
 #include "hlr_common.hpp"
@@ -14,5 +14,8 @@ struct bf16 {
     return __builtin_bit_cast(float, static_cast<uint32_t>(bits) << 16);
   }
 };
+
+// Blocks of one launch: HIP takes fewer than 2^32 threads, so larger calls are several launches.
+constexpr int64_t most_blocks(int threads) { return 0xffffffffll / threads; }
 
 }  // namespace hlr

@@ -74,6 +74,7 @@ struct SampleArgs {
   int64_t items;
   int64_t *index;
   float *logprob;
+  int64_t first;  // row of this launch's first block
 };
 
 // What a row's items are measured against.
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   __shared__ uint64_t tmp[17];
   __shared__ int listed;
   constexpr int kCap = sizeof(list) / 8;
-  const int64_t r = blockIdx.x;
+  const int64_t r = a.first + blockIdx.x;
   const int tid = threadIdx.x, items = static_cast<int>(a.items);
   const T *x = static_cast<const T *>(a.scores) + r * a.stride;
   const float *noise = a.noise + r * a.noise_stride;
@@ -947,23 +948,28 @@ __global__ void __launch_bounds__(NT) sample_kernel(SampleArgs a) {
   }
 }
 
+template <typename T, int NT, bool kOne>
+hlr_status launch_rows(SampleArgs a, int64_t rows, hipStream_t stream) {
+  for (; a.first < rows; a.first += most_blocks(NT)) {
+    const int64_t here = rows - a.first < most_blocks(NT) ? rows - a.first : most_blocks(NT);
+    sample_kernel<T, NT, kOne><<<static_cast<unsigned>(here), NT, 0, stream>>>(a);
+    const hlr_status st = launch_status();
+    if (st != HLR_OK) return st;
+  }
+  return HLR_OK;
+}
+
 // Threads by the row's length: one item per thread where the row is that
 // short; 512 up to 8,192 items (64 rows of 8,192 fp16: top-k 50 12 us, 16 with 1,024; top-p
 // 0.95 27 and 35), 1,024 beyond (128 rows of 16,384 fp32: top-k 900 29 us, 42 with 512; the
 // others within 12%).
 template <typename T>
-void launch(const SampleArgs &a, int64_t rows, hipStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(rows);
-  if (a.items <= 256)
-    sample_kernel<T, 256, true><<<grid, 256, 0, stream>>>(a);
-  else if (a.items <= 512)
-    sample_kernel<T, 512, true><<<grid, 512, 0, stream>>>(a);
-  else if (a.items <= 1024)
-    sample_kernel<T, 1024, true><<<grid, 1024, 0, stream>>>(a);
-  else if (a.items <= 8192)
-    sample_kernel<T, 512, false><<<grid, 512, 0, stream>>>(a);
-  else
-    sample_kernel<T, 1024, false><<<grid, 1024, 0, stream>>>(a);
+hlr_status launch(const SampleArgs &a, int64_t rows, hipStream_t stream) {
+  if (a.items <= 256) return launch_rows<T, 256, true>(a, rows, stream);
+  if (a.items <= 512) return launch_rows<T, 512, true>(a, rows, stream);
+  if (a.items <= 1024) return launch_rows<T, 1024, true>(a, rows, stream);
+  if (a.items <= 8192) return launch_rows<T, 512, false>(a, rows, stream);
+  return launch_rows<T, 1024, false>(a, rows, stream);
 }
 
 }  // namespace
@@ -980,12 +986,8 @@ extern "C" hlr_status sample_scores(const void *scores, int32_t type, int64_t ro
   if (!aligned(scores, type == HLR_FP32 ? 4 : 2) || !aligned(noise, 4) || !aligned(temperature, 4) ||
       !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(out_index, 8) || !aligned(out_logprob, 4))
     return HLR_MISALIGNED;
-  const SampleArgs a{scores, stride, noise, noise_stride, temperature, top_k, top_p, min_p, items, out_index, out_logprob};
-  if (type == HLR_FP32)
-    launch<float>(a, rows, stream);
-  else if (type == HLR_BF16)
-    launch<bf16>(a, rows, stream);
-  else
-    launch<_Float16>(a, rows, stream);
-  return launch_status();
+  const SampleArgs a{scores, stride, noise, noise_stride, temperature, top_k, top_p, min_p, items, out_index, out_logprob, 0};
+  if (type == HLR_FP32) return launch<float>(a, rows, stream);
+  if (type == HLR_BF16) return launch<bf16>(a, rows, stream);
+  return launch<_Float16>(a, rows, stream);
 }

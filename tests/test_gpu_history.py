@@ -637,6 +637,60 @@ def test_scales_of_blocks_that_nobody_sees_may_be_anything(dev, D, group, new):
             assert torch.equal(got, want) and torch.equal(gl, wl), bad
 
 
+def test_append_and_read_beyond_one_launch(dev):
+    """More blocks than the 2^32 threads of a launch hold: 130 spans of 64 tokens, keys and values of 65,535 heads."""
+    heads, B, D, n = 65535, 16, 32, 64 * 129 + 10
+    g = torch.Generator(device=dev)
+    g.manual_seed(51)
+    x = torch.randn((2, n, 1, D), generator=g, device=dev).to(torch.bfloat16)
+    slots = torch.full((n,), -1, dtype=torch.int64, device=dev)
+    real = [10, 8190, 8191, 8192, 8193, 8260, n - 1]  # spans 0, 127, 128 and 129; a run over the border of the launches
+    slots[real] = torch.tensor([17, 32, 33, 34, 35, 0, 50], device=dev)
+    pools = []
+    for h in (heads, 2):
+        pool = [torch.zeros((4, h, B, D), dtype=torch.int8, device=dev), torch.zeros((4, h, 1, D, 16), dtype=torch.int8, device=dev),
+                torch.zeros((4, h), device=dev), torch.zeros((4, h), device=dev)]
+        hlr.hist_append(*pool, x[0].expand(n, h, D), x[1].expand(n, h, D), slots)
+        pools.append(pool)
+    for big, small in zip(*pools):
+        assert bool((big == small[:, :1]).all()) and bool(small.any())
+    want = hlr.hist_read(*pools[1], slots, dtype=torch.bfloat16)
+    got = hlr.hist_read(*pools[0], slots, dtype=torch.bfloat16)
+    for a, b in zip(got, want):
+        for t in real + [0, 11, 8189, 8194, n - 2]:
+            assert bool((a[t] == b[t, :1]).all()) and bool(b[t].any()) == (t in real)
+    del got, a
+    torch.cuda.empty_cache()
+
+
+def test_attention_beyond_one_launch(dev):
+    """More blocks than the 2^32 threads of a launch hold, over requests and over the joined rows."""
+    R, D = 65535, 32
+    cache = Cache(dev, [16] * 9, 1, 16, D, 53)
+    g = torch.Generator(device=dev)
+    g.manual_seed(54)
+    q = torch.randn((R, 1, D), generator=g, device=dev).to(torch.bfloat16)
+    table = torch.randint(0, 9, (R, 1), generator=g, device=dev).to(torch.int32)
+    lengths = torch.randint(0, 17, (R,), generator=g, device=dev).to(torch.int32)
+    cu = torch.arange(R + 1, dtype=torch.int32, device=dev)
+    max_q = 128 * 256 + 1  # 257 blocks of rows for each request
+    out, lse = hlr.hist_attention(q, *cache.tensors(), table, lengths, cu, max_q, 16, return_lse=True)
+    for a, b in ((0, 30_000), (30_000, R)):
+        want, wl = hlr.hist_attention(q[a:b], *cache.tensors(), table[a:b], lengths[a:b], cu[:b - a + 1], max_q, 16,
+                                      return_lse=True)
+        assert torch.equal(out[a:b], want) and torch.equal(lse[a:b], wl)
+    cache = Cache(dev, [1100, 1], 1, 16, D, 55)
+    n = (1 << 22) + 10
+    q = torch.zeros((n, 4, D), dtype=torch.bfloat16, device=dev)  # all but the last two tokens belong to no request
+    q[-2:] = queries(dev, 2, 4, D, "bf16", 56)
+    want, wl = check(cache, q[-2:], [0, 1, 2])
+    ws = hlr.new_workspace(dev, hlr.hist_attention_workspace_size(n, 2, 4, 1, D, 1, 1100))
+    got, gl = hlr.hist_attention(q, *cache.tensors(), cache.table, cache.lengths,
+                                 torch.tensor([n - 2, n - 1, n], dtype=torch.int32, device=dev), 1, 1100, return_lse=True,
+                                 ws=ws)
+    assert torch.equal(got[-2:], want) and torch.equal(gl[-2:], wl)
+
+
 # --------------------------------------------------------------- refusals
 def test_refusals(dev):
     cache = Cache(dev, [20, 20], 2, 16, 64, 27)

@@ -246,6 +246,17 @@ def test_frequencies(dev):
     assert float(((got - want)[kept] ** 2 / want[kept]).sum()) < 27.9  # chi-square, 3 degrees, 4e-6
 
 
+def test_more_rows_than_a_launch_has_blocks(dev):
+    """2^22 blocks of 1,024 threads pass the 2^32 threads of one launch."""
+    rows, items = (1 << 22) + 5, 600
+    x = torch.zeros((1, items), device=dev).expand(rows, items)
+    e = (1.0 / torch.arange(1, items + 1, device=dev))[None].expand(rows, items)  # of equal scores the last one kept wins
+    k = 1 + torch.arange(rows, device=dev, dtype=torch.int32) % 577
+    index, logprob = hlr.sample_scores(x, e, top_k=k)
+    assert torch.equal(index, k.long() - 1)
+    assert float((logprob + math.log(items)).abs().max()) <= 2.0 ** -22 * (4 + math.log(items))
+
+
 def test_refusals(dev):
     x, e = inputs(dev, 4, 100, "fp32", 15)
     with pytest.raises(hlr.HLRError):
