@@ -181,3 +181,49 @@ def test_a_stream_of_its_own_is_ordered_with_the_callers(dev, return_lse):
     assert len(want) == len(got)
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+def test_calls_do_not_wait_for_the_gpu(dev):
+    """A pool of more than a million blocks and a history of 600,000 events, with a third of a second of work queued."""
+    cache = HistoryCache(3, 1_200_000, 1, 32, 700_000, dev, block=16)
+    kv = torch.randn((600_000, 1, 32), device=dev)
+    cache.append(kv, kv, [5, 0, 599_995])
+    k, _ = cache.read(2)
+    cache.attend(kv[:2], counts=[1, 0, 1])
+    busy = torch.randn((8192, 8192), device=dev).to(torch.bfloat16)
+    busy @ busy
+    torch.cuda.synchronize()
+    for _ in range(400):
+        busy @ busy
+    done = torch.cuda.Event()
+    done.record()
+    again, _ = cache.read(2)
+    cache.release(2)
+    cache.append(kv[:70], kv[:70], [0, 30, 40])
+    cache.attend(kv[:2], counts=[1, 0, 1])
+    assert not done.query()
+    torch.cuda.synchronize()
+    assert torch.equal(k, again) and cache.held == [5, 30, 40]
+    # a step is at most 1/127 of a block's largest value, a code half a step off
+    assert float((k - kv[5:]).abs().max()) <= 0.5001 / 127 * float(kv.abs().max())
+
+
+def test_the_free_list_outlasts_many_releases(dev):
+    """Blocks handed out and given back for longer than the list's room on the GPU: table and host agree."""
+    users, B = 4, 16
+    cache = HistoryCache(users, 9, 1, 32, 120, dev, block=B)
+    kv = torch.randn((300, 1, 32), device=dev)
+    g = torch.Generator()
+    g.manual_seed(3)
+    for step in range(60):
+        u = int(torch.randint(0, users, (1,), generator=g))
+        cache.release(u)
+        new = [0] * users
+        new[u] = min(int(torch.randint(0, 61, (1,), generator=g)), cache.free_blocks * B)
+        cache.append(kv[:sum(new)], kv[:sum(new)], new)
+        assert sorted(cache._free + sum(cache.blocks, [])) == list(range(9))
+        for v in range(users):
+            assert cache.table[v, :len(cache.blocks[v])].tolist() == cache.blocks[v]
+            assert not (cache.table[v, len(cache.blocks[v]):] != -1).any()
+        assert torch.equal(cache.read(u)[0], hlr.hist_read(*cache.tensors(), torch.tensor(
+            [b * B + i for b in cache.blocks[u] for i in range(B)][:new[u]], dtype=torch.int64, device=dev))[0])
