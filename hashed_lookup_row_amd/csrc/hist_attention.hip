@@ -14,10 +14,13 @@
 // bytes of [chunk][d][16].
 //
 // Precision: a query row is multiplied by a power of two that brings its
-// largest magnitude to [512, 1024), so bf16 and f16 queries are exact in f16
-// (fp32 ones are split into two f16 parts).  Scores, the running maximum and
+// largest magnitude to [512, 1024), so elements of bf16 and f16 queries down to
+// 2^-23 of it are exact in f16, smaller ones off by at most 2^-34 of it (fp32 ones
+// are split into two f16 parts, 22 bits).  Scores, the running maximum and
 // sum, and the output are fp32.  The weights p are one f16 part for bf16
-// outputs and two for fp16 and fp32: at 11 bits their own rounding would be as
+// outputs (the error against 64 bits is 1.671e-3 with one and 1.660e-3, the output's own
+// rounding, with two, which take 29% longer in a causal prompt and 41% for candidates) and two for
+// fp16 and fp32: at 11 bits their own rounding would be as
 // large as fp16's (the error against 64 bits 1.4 to 1.5 times what the output's rounding gives).  A
 // weight enters the second product times its chunk's value scale, relative to
 // the row's largest such product so far and times 2^12, which keeps terms
@@ -103,8 +106,9 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 // A tile of 64 tokens as f16 in LDS, in units of 16 bytes: keys as rows (t, m)
 // of D/8 units, token(t, m) as above; values as rows d of 8 units (unit 2 g + u:
 // tokens 8 u .. 8 u + 7 of chunk g).  A read takes one unit of 16
-// successive rows; the units of a row are permuted (xor) so that any eight of
-// those lie in different banks.
+// successive rows; the units of a row are permuted (xor) so that those of eight
+// successive rows lie in different banks.  (Conflicts still take 24 to 38% of the LDS's
+// cycles, so a 16-byte access does not go by eight neighbouring lanes alone.)
 template <int D>
 struct RowTile {  // D = 64, 128, 256
   static constexpr int kUnits = D / 8, kKeys = 64 * kUnits, kValues = D * 8;  // units of a key row, of both tiles
@@ -428,9 +432,10 @@ __device__ __forceinline__ void store_rows(const Args &a, Wave<T, D, NQ> &w, int
 // Many rows: each of the four waves has 16 NQ of them and all walk the same
 // tiles.  A tile is fetched and turned into f16 once per block, a quarter by
 // each wave, into one of two LDS buffers: while a tile is worked on, the codes of
-// the next are in flight to registers, and go to the other buffer between its two products.  Bound by the VALU work
-// beside the products (softmax, conversion; the matrix cores are busy a quarter of the time): 8 requests of up to 2,048
-// new on up to 2,047 cached, causal, 16 heads of 128: 300 us, 610 TFLOP/s (668 us with every wave converting for
+// the next are in flight to registers, and go to the other buffer between its two products.  No unit is
+// full: VALU (softmax, conversion) 44% of the cycles (64% at D = 64), matrix cores 21 to 24%, waves waiting 31 to 35%; a
+// wave's products, softmax and conversion follow one another, and two or three waves of a SIMD take turns.  The kernel alone: 8 requests of up to
+// 2,048 new on up to 2,047 cached, causal, 16 heads of 128: 318 us, 580 TFLOP/s (668 us with every wave converting for
 // itself); 64 x 1,024 candidates, 8 heads of 64: 271 us, 515 TFLOP/s.
 template <typename T, int D, int NQ>
 __global__ void __launch_bounds__(kWaves *kWave, D <= 128 ? 2 : 1) rows_kernel(Args a) {

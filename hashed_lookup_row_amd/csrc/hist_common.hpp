@@ -15,7 +15,8 @@ struct bf16 {
   }
 };
 
-// Blocks of one launch: HIP takes fewer than 2^32 threads, so larger calls are several launches.
+// Blocks of one launch: it holds fewer than 2^32 threads (more wrap around without an error: 2^22 + 5 blocks of 1,024 ran
+// as 5), so larger calls are several launches.
 constexpr int64_t most_blocks(int threads) { return 0xffffffffll / threads; }
 
 }  // namespace hlr

@@ -643,9 +643,10 @@ hlr_status hist_read(const int8_t *k_codes, const int8_t *v_codes, const float *
  *  out[tokens][q_heads][dim] of q's type; out_lse[tokens][q_heads] fp32,
  *  nullable: the natural logarithm of the sum of exp(scale q k).  Tokens of no
  *  request are not written.
- *  Scores, softmax statistics and sums are fp32; the softmax weights are
- *  rounded to 11 bits before the product with the values for HLR_BF16, and to
- *  22 bits for the other types.
+ *  Scores, softmax statistics and sums are fp32; HLR_FP32 queries are rounded
+ *  to 22 bits, any query's elements to 2^-34 of the largest of their row; the
+ *  softmax weights are rounded to 11 bits before the product with the values
+ *  for HLR_BF16, and to 22 bits for the other types.
  *  Workspace: hist_attention_workspace_size(...) bytes. */
 size_t hist_attention_workspace_size(int64_t tokens, int64_t requests, int64_t q_heads, int64_t kv_heads, int64_t dim,
                                      int64_t max_q, int64_t max_len);
@@ -673,6 +674,8 @@ hlr_status hist_attention(const void *q, int32_t type, int64_t tokens, int64_t q
  *  out_index[rows] int64; -1 if no item can be drawn.  out_logprob[rows]: the
  *  logarithm of the drawn item's share of the mass of all items, before the
  *  filters (for temperature 0 that of temperature 1); -inf with index -1.
+ *  Masses are held in 32 bits: where the edge of top_p lies may be off by
+ *  items * 2^-32 of all mass.
  *  items at most HLR_SAMPLE_MAX_ITEMS.
  * --------------------------------------------------------------------- */
 #define HLR_SAMPLE_MAX_ITEMS (1 << 27)
